@@ -127,7 +127,7 @@
 extern "C" {
 #endif
 
-#define SA_ABI_VERSION 4
+#define SA_ABI_VERSION 5
 
 typedef enum sa_status {
   SA_OK = 0,
@@ -381,6 +381,144 @@ sa_status sa_indexer_kl_grad(const sa_indexer_args* args, const sa_indexer_grads
  * o, d_o bf16 [.., Hq, d_v]; delta fp32 [.., Hq] (device).  Asynchronous. */
 sa_status sa_softmax_grad_preprocess(const sa_args* args, const void* o, const void* d_o,
                                      float* delta, void* stream);
+
+/* ---- serving over a paged KV cache held in 8 bits ------------------------ */
+
+/* Three calls, in the order of a serving step: sa_page_plan hands pages to the
+ * requests of a step and lists where their new tokens lie, sa_kv8_write rounds the
+ * new K and V rows to 8 bits into those pages, sa_kv8_fwd attends to the pages.
+ *
+ * The cache.  Codes k [n_pages, page_size, Hkv, d_qk] and v [n_pages, page_size,
+ * Hkv, d_v] of one byte each, and one fp32 scale per page and head, k_scale and
+ * v_scale [n_pages, Hkv]: an element is its code times its page's scale.  With
+ * kv_shared there is k alone, and V is the first d_v columns of its rows.  Logical
+ * row r of sequence b lies in page block_table[b, r / page_size] at r % page_size.
+ * Scales are read as clamped to [2^-60, 2^60] (NaN as 2^-60).
+ *
+ * The tokens.  Sequence b has the packed tokens [cu_seqlens_q[b], cu_seqlens_q[b+1])
+ * (TND) or its s_q tokens (BSND), and they are its last rows: with n tokens and
+ * L = seq_lens[b], token i stands at row L - n + i.  Rows behind the last sequence
+ * are neither read nor written.  L is clamped to max_pages * page_size; a token at a
+ * negative row sees nothing and is not written.
+ *
+ * Status.  `status` (device int32, optional) gets the bits of the status word above
+ * ORed in: 1 when a page or block index inside a sequence lies outside the cache or
+ * the sequence (it selects nothing, and nothing is written through it).  The
+ * library never clears it.  sa_read_status(status, 4, stream) reads and maps it. */
+typedef enum sa_kv8_format {
+  SA_KV8_E4M3 = 0,  /* e4m3 (no infinities; +-448 the largest) */
+  SA_KV8_INT8 = 1   /* integers in [-127, 127] */
+} sa_kv8_format;
+
+typedef struct sa_kv8_cache {
+  int32_t format;          /* sa_kv8_format */
+  int32_t n_heads_kv;      /* Hkv */
+  int32_t d_qk, d_v;       /* 64/64, 128/128, 192/128; kv_shared: 128/128, 576/512 */
+  int32_t kv_shared;       /* 1: V is the first d_v columns of k; v and v_scale are unused */
+  int32_t page_size;       /* rows per page */
+  int32_t n_pages;         /* pages in the cache */
+  int32_t batch;           /* B sequences */
+  int32_t max_pages;       /* pages per sequence in block_table */
+  int32_t layout;          /* sa_layout of the tokens */
+  int32_t s_q;             /* BSND: tokens per sequence */
+  int32_t t_q;             /* TND: rows of the packed token axis */
+  int64_t table_stride;    /* elements from one sequence's block_table row to the next */
+  void* k;                 /* codes, 16-byte aligned (sa_kv8_fwd reads them, sa_kv8_write writes them) */
+  void* v;
+  float* k_scale;          /* [n_pages, Hkv] */
+  float* v_scale;
+  const int32_t* block_table;   /* [B, max_pages] */
+  const int32_t* seq_lens;      /* [B] rows of each sequence, its new tokens included */
+  const int32_t* cu_seqlens_q;  /* TND: B + 1 offsets */
+  int32_t* status;              /* optional */
+} sa_kv8_cache;
+
+/* The plan of a step.  Request b holds old_lens[b] rows in the first
+ * ceil(old_lens[b] / page_size) entries of its block_table row and adds new_lens[b]
+ * tokens.  Requests are served in order, up to the first that does not fit: its
+ * lengths are negative, its pages exceed max_pages, the tokens so far exceed
+ * n_tokens, or the free pages run out.  From that one on nothing is planned: no
+ * tokens, no pages, seq_lens = old_lens.  A page needed is taken from the end of the
+ * stack free_pages[0 .. n_free): request by request, then page by page.
+ * Outputs: the new entries of block_table; seq_lens [B] = old + new;
+ * cu_seqlens_q [B + 1]; slots [n_tokens], the cache row (page * page_size + offset)
+ * of each packed token, -1 behind the last served one and where an entry of the
+ * table that should hold a page is negative; n_free_out [1], what is left of the
+ * stack; n_served [1].  The free list itself is not written. */
+typedef struct sa_page_plan_args {
+  int32_t batch;           /* B, at most 24576 */
+  int32_t max_pages;
+  int32_t page_size;
+  int32_t n_tokens;        /* capacity of slots */
+  int32_t free_capacity;   /* elements of free_pages; n_free is clamped to it */
+  int64_t table_stride;
+  const int32_t* old_lens;    /* [B] */
+  const int32_t* new_lens;    /* [B] */
+  const int32_t* free_pages;
+  const int32_t* n_free;      /* [1] */
+  int32_t* block_table;       /* [B, max_pages], updated */
+  int32_t* seq_lens;          /* [B]; no input's buffer */
+  int32_t* cu_seqlens_q;      /* [B + 1] */
+  int64_t* slots;             /* [n_tokens] */
+  int32_t* n_free_out;        /* [1]; no input's buffer */
+  int32_t* n_served;          /* [1] */
+} sa_page_plan_args;
+
+/* Errors: SA_ERR_NULLPTR, SA_ERR_PARAM (sizes; an output in an input's buffer).
+ * One kernel, no workspace.  Asynchronous. */
+sa_status sa_page_plan(const sa_page_plan_args* args, void* stream);
+
+/* New rows to write: k [.., Hkv, d_qk] and v [.., Hkv, d_v] of the element type
+ * `dtype`, a token's row contiguous, `*_stride` elements from token to token. */
+typedef struct sa_kv8_rows {
+  int32_t dtype;           /* sa_dtype */
+  const void* k;
+  const void* v;           /* unused with kv_shared */
+  int64_t k_stride, v_stride;  /* multiples of 8 */
+} sa_kv8_rows;
+
+/* Write the step's tokens into their pages.  For each page and head that gets rows,
+ * with a the largest finite magnitude among them, the page's scale becomes
+ *   s = the least power of two with a <= top * s   (top 448 or 127; at least 2^-60,
+ *       at most 2^60),
+ * or, when the page holds rows before the first new one, the larger of that and the
+ * scale it has (raised to a power of two); those rows' codes are then rounded again
+ * to the new scale where it changed (e4m3: exact short of subnormals, since the
+ * ratio is a power of two).  A code is x / s rounded to nearest even and saturated;
+ * NaN becomes the e4m3 NaN, or 0 in integers.  Two sequences must not write rows of
+ * one page in the same call (the page's result is then undefined).
+ * Errors: SA_ERR_NULLPTR, SA_ERR_PARAM, SA_ERR_UNSUPPORTED (head sizes not built).
+ * One kernel, no workspace.  Asynchronous. */
+sa_status sa_kv8_write(const sa_kv8_cache* cache, const sa_kv8_rows* rows, void* stream);
+
+/* Queries and outputs of the attention over the cache. */
+typedef struct sa_kv8_query {
+  int32_t dtype;           /* sa_dtype of q and o */
+  int32_t n_heads_q;       /* Hq, a multiple of Hkv */
+  int32_t block_size;      /* rows per index */
+  int32_t topk;            /* index slots per (token, kv-head); 0: every row */
+  int64_t win_left;        /* rows before the token's own that it sees; -1: all */
+  float scale;             /* multiplies Q K^T */
+  uint32_t flags;          /* 0 */
+  const void* q;           /* [.., Hq, d_qk] */
+  int64_t q_stride;        /* elements from token to token, a multiple of 8 */
+  const int32_t* idx;      /* [.., Hkv, topk] block (or row) indices local to the sequence, negative = empty */
+  const int32_t* topk_len; /* optional [.., Hkv]: usable slots */
+  const float* sinks;      /* optional [Hq] sink logits */
+  void* o;                 /* [.., Hq, d_v], contiguous */
+  float* lse;              /* [.., Hq] */
+} sa_kv8_query;
+
+/* O = softmax(scale Q K^T [, sink]) V and lse over the rows that a token selects (all,
+ * or those of its indices, an index named twice counting twice) and sees: row r of
+ * the token at row ta is visible for ta - win_left <= r <= ta.  A row that a token
+ * does not see has no part in its result, whatever the row holds.  A token with no
+ * visible row and no sink gets lse = +inf and O = 0.
+ * Errors: SA_ERR_NULLPTR, SA_ERR_PARAM, SA_ERR_UNSUPPORTED, SA_ERR_WORKSPACE.
+ * The workspace needs no initial contents; calls that may overlap on the GPU need
+ * one each.  Asynchronous. */
+sa_status sa_kv8_fwd_get_workspace_size(const sa_kv8_cache* cache, const sa_kv8_query* query, size_t* ws_bytes);
+sa_status sa_kv8_fwd(const sa_kv8_cache* cache, const sa_kv8_query* query, void* ws, size_t ws_bytes, void* stream);
 
 /* ---- inspection ------------------------------------------------------- */
 

@@ -29,6 +29,8 @@ SA_MASK_CAUSAL = 1
 SA_MASK_BAND = 2
 SA_DTYPE_BF16 = 0
 SA_DTYPE_FP16 = 1
+SA_KV8_E4M3 = 0
+SA_KV8_INT8 = 1
 SA_FLAG_CHECK = 1
 SA_FLAG_QUERY_STATIONARY_BWD = 2
 SA_FLAG_DQ_SEPARATE = 4
@@ -95,6 +97,40 @@ class SaIndexerGrads(ctypes.Structure):
     _fields_ = [("loss", _vp), ("dq", _vp), ("dk", _vp), ("dw", _vp)]
 
 
+class SaKv8Cache(ctypes.Structure):
+    _fields_ = [
+        ("format", ctypes.c_int32), ("n_heads_kv", ctypes.c_int32), ("d_qk", ctypes.c_int32), ("d_v", ctypes.c_int32),
+        ("kv_shared", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+        ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("layout", ctypes.c_int32),
+        ("s_q", ctypes.c_int32), ("t_q", ctypes.c_int32), ("table_stride", ctypes.c_int64),
+        ("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("block_table", _vp), ("seq_lens", _vp),
+        ("cu_seqlens_q", _vp), ("status", _vp),
+    ]
+
+
+class SaKv8Rows(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("k", _vp), ("v", _vp), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
+
+
+class SaKv8Query(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("n_heads_q", ctypes.c_int32), ("block_size", ctypes.c_int32),
+        ("topk", ctypes.c_int32), ("win_left", ctypes.c_int64), ("scale", ctypes.c_float), ("flags", ctypes.c_uint32),
+        ("q", _vp), ("q_stride", ctypes.c_int64), ("idx", _vp), ("topk_len", _vp), ("sinks", _vp), ("o", _vp),
+        ("lse", _vp),
+    ]
+
+
+class SaPagePlanArgs(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("n_tokens", ctypes.c_int32), ("free_capacity", ctypes.c_int32), ("table_stride", ctypes.c_int64),
+        ("old_lens", _vp), ("new_lens", _vp), ("free_pages", _vp), ("n_free", _vp), ("block_table", _vp),
+        ("seq_lens", _vp), ("cu_seqlens_q", _vp), ("slots", _vp), ("n_free_out", _vp), ("n_served", _vp),
+    ]
+
+
 class SaFwdOut(ctypes.Structure):
     _fields_ = [("o", _vp), ("lse", _vp)]
 
@@ -119,7 +155,8 @@ EXPORTS = ["sa_fwd_get_workspace_size", "sa_fwd", "sa_bwd_get_workspace_size", "
            "sa_bwd_no_alloc_max_workspace", "sa_selftest_mma", "sa_selftest_wait_timeout",
            "sa_selftest_mma2", "sa_plan", "sa_read_status", "sa_bwd_no_alloc_read_status",
            "sa_debug_block_index", "sa_selftest_gather4", "sa_softmax_l1norm",
-           "sa_indexer_kl_grad_get_workspace_size", "sa_indexer_kl_grad"]
+           "sa_indexer_kl_grad_get_workspace_size", "sa_indexer_kl_grad", "sa_page_plan", "sa_kv8_write",
+           "sa_kv8_fwd_get_workspace_size", "sa_kv8_fwd"]
 
 
 def lib() -> ctypes.CDLL:
@@ -139,6 +176,10 @@ def lib() -> ctypes.CDLL:
         L.sa_softmax_l1norm.argtypes = [P(SaArgs), _vp, _vp, _vp, _vp]
         L.sa_indexer_kl_grad_get_workspace_size.argtypes = [P(SaIndexerArgs), P(ctypes.c_size_t)]
         L.sa_indexer_kl_grad.argtypes = [P(SaIndexerArgs), P(SaIndexerGrads), _vp, ctypes.c_size_t, _vp]
+        L.sa_page_plan.argtypes = [P(SaPagePlanArgs), _vp]
+        L.sa_kv8_write.argtypes = [P(SaKv8Cache), P(SaKv8Rows), _vp]
+        L.sa_kv8_fwd_get_workspace_size.argtypes = [P(SaKv8Cache), P(SaKv8Query), P(ctypes.c_size_t)]
+        L.sa_kv8_fwd.argtypes = [P(SaKv8Cache), P(SaKv8Query), _vp, ctypes.c_size_t, _vp]
         L.sa_debug_resolve.argtypes = [P(SaArgs), _vp, _vp, ctypes.c_int32, _vp]
         L.sa_status_string.argtypes = [ctypes.c_int32]
         L.sa_status_string.restype = ctypes.c_char_p
@@ -247,6 +288,25 @@ def sa_indexer_kl_grad(args: SaIndexerArgs, grads: SaIndexerGrads, ws: int, ws_b
 
 def sa_softmax_l1norm(args: SaArgs, lse: int, ori_out, cmp_out, stream: int = 0) -> None:
     _check(lib().sa_softmax_l1norm(ctypes.byref(args), lse, ori_out, cmp_out, stream), "sa_softmax_l1norm")
+
+
+def sa_page_plan(args: SaPagePlanArgs, stream: int = 0) -> None:
+    _check(lib().sa_page_plan(ctypes.byref(args), stream), "sa_page_plan")
+
+
+def sa_kv8_write(cache: SaKv8Cache, rows: SaKv8Rows, stream: int = 0) -> None:
+    _check(lib().sa_kv8_write(ctypes.byref(cache), ctypes.byref(rows), stream), "sa_kv8_write")
+
+
+def sa_kv8_fwd_get_workspace_size(cache: SaKv8Cache, query: SaKv8Query) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().sa_kv8_fwd_get_workspace_size(ctypes.byref(cache), ctypes.byref(query), ctypes.byref(n)),
+           "sa_kv8_fwd_get_workspace_size")
+    return n.value
+
+
+def sa_kv8_fwd(cache: SaKv8Cache, query: SaKv8Query, ws, ws_bytes: int, stream: int = 0) -> None:
+    _check(lib().sa_kv8_fwd(ctypes.byref(cache), ctypes.byref(query), ws, ws_bytes, stream), "sa_kv8_fwd")
 
 
 def sa_debug_resolve(args: SaArgs, rows: int, counts: int, max_rows: int, stream: int = 0) -> None:

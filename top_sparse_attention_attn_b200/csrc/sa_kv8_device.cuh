@@ -1,0 +1,73 @@
+// sa_kv8_device.cuh -- device helpers of the 8-bit paged cache: tokens and
+// pages, scales, and the conversions between codes and 16-bit floats.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "sa_device.cuh"
+#include "sa_kv8.h"
+
+namespace sa {
+
+// Scales as the kernels use them: [2^-60, 2^60], NaN as 2^-60 (fmaxf drops it).
+__device__ __forceinline__ float k8_scale(float s) { return fminf(fmaxf(s, 0x1p-60f), 0x1p60f); }
+
+// The tokens of sequence b: [t0, t0 + n), its rows L, and the row of its first token.
+struct K8Seq {
+  int t0, n, L, first;
+};
+__device__ __forceinline__ int k8_cu(const K8Cache& c, int b) {
+  return c.cu ? min(max(__ldg(c.cu + b), 0), c.T) : b * c.s_q;
+}
+__device__ __forceinline__ int k8_len(const K8Cache& c, int b) {
+  return min(max(__ldg(c.lens + b), 0), c.max_pages * c.ps);
+}
+__device__ __forceinline__ K8Seq k8_seq(const K8Cache& c, int b) {
+  K8Seq s;
+  s.t0 = k8_cu(c, b);
+  s.n = max(k8_cu(c, b + 1) - s.t0, 0);
+  s.L = k8_len(c, b);
+  s.first = s.L - s.n;
+  return s;
+}
+// The sequence of token t (the largest b with cu[b] <= t); the caller checks that t lies inside it.
+__device__ __forceinline__ int k8_find(const K8Cache& c, int t) { return c.cu ? find_batch(c.cu, c.B, t) : t / c.s_q; }
+
+// The page that holds a row of sequence b, or -1 (index bit raised) when the table
+// names none of the cache.  0 <= row < max_pages * ps.
+__device__ __forceinline__ int k8_page(const K8Cache& c, int b, int row) {
+  const int p = __ldg(c.table + b * c.tstride + row / c.ps);
+  if (p >= 0 && p < c.n_pages) return p;
+  if (c.status) atomicOr(c.status, kStatusIndexRange);
+  return -1;
+}
+
+__device__ __forceinline__ float k8_in(const void* p, long long i, int f16) {
+  return f16 ? __half2float(static_cast<const __half*>(p)[i]) : __bfloat162float(static_cast<const bf16*>(p)[i]);
+}
+
+// Two e4m3 codes (low byte first) -> two halves; exact.
+__device__ __forceinline__ uint32_t k8_e4m3x2(uint32_t two) {
+  uint32_t r;
+  asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(r) : "r"(two));
+  return r;
+}
+__device__ __forceinline__ float k8_code(uint8_t c, int fmt) {
+  if (fmt == kFmtInt8) return (float)(int8_t)c;
+  const uint32_t h = k8_e4m3x2(c);
+  return __half2float(__ushort_as_half((unsigned short)h));
+}
+// Two floats -> two codes, rounded to nearest even and saturated.  NaN: the e4m3 NaN, 0 in integers.
+__device__ __forceinline__ uint32_t k8_round2(float lo, float hi, int fmt) {
+  if (fmt == kFmtInt8) {
+    const int a = __float2int_rn(fminf(fmaxf(lo, -127.f), 127.f)), b = __float2int_rn(fminf(fmaxf(hi, -127.f), 127.f));
+    return (uint32_t)((lo == lo ? a : 0) & 255) | ((uint32_t)((hi == hi ? b : 0) & 255) << 8);
+  }
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+}  // namespace sa

@@ -1,0 +1,277 @@
+// sa_kv8_write.cu -- the page plan of a serving step and the write that rounds
+// new K / V rows to 8 bits into the pages (sa_page_plan, sa_kv8_write).
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "sa_kv8_device.cuh"
+#include "sa_launch.h"
+
+namespace sa {
+
+// ---------------------------------------------------------------------------
+// page plan
+// ---------------------------------------------------------------------------
+// One launch.  Every block scans the requests' lengths itself (8 bytes a request,
+// from L2) into two prefix arrays in shared memory, tokens and new pages, and then
+// looks up its share of the tokens and new pages there by bisection; block 0 writes
+// the per-request outputs.  The scan repeated per block costs less than a second
+// launch that would wait for it.
+__device__ __forceinline__ int plan_upper(const int* a, int n, int x) {  // largest b < n with a[b] <= x
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void page_plan_kernel(PagePlan p) {
+  extern __shared__ int sm[];
+  int* cu = sm;                // [B + 1]
+  int* pg = sm + p.B + 1;      // [B + 1]
+  __shared__ long long wtok[32], wpage[32];
+  __shared__ int fail;
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int n_free = min(max(__ldg(p.n_free), 0), p.free_cap);
+  if (tid == 0) fail = p.B;
+  const int per = (p.B + nt - 1) / nt, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  // sums of this thread's requests (64 bits: the lengths are the caller's)
+  long long tok = 0, page = 0;
+  for (int b = b0; b < b1; ++b) {
+    const long long o = __ldg(p.old_lens + b), n = __ldg(p.new_lens + b);
+    if (o < 0 || n < 0) continue;
+    tok += n;
+    page += (o + n + p.ps - 1) / p.ps - (o + p.ps - 1) / p.ps;
+  }
+  long long it = tok, ip = page;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long a = __shfl_up_sync(~0u, it, d), b = __shfl_up_sync(~0u, ip, d);
+    if (lane >= d) { it += a; ip += b; }
+  }
+  if (lane == 31) { wtok[warp] = it; wpage[warp] = ip; }
+  __syncthreads();
+  if (warp == 0) {
+    long long a = lane < (nt >> 5) ? wtok[lane] : 0, b = lane < (nt >> 5) ? wpage[lane] : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long x = __shfl_up_sync(~0u, a, d), y = __shfl_up_sync(~0u, b, d);
+      if (lane >= d) { a += x; b += y; }
+    }
+    wtok[lane] = a;
+    wpage[lane] = b;
+  }
+  __syncthreads();
+  long long ct = it - tok + (warp ? wtok[warp - 1] : 0), cp = ip - page + (warp ? wpage[warp - 1] : 0);
+  int bad = p.B;
+  for (int b = b0; b < b1; ++b) {
+    const long long o = __ldg(p.old_lens + b), n = __ldg(p.new_lens + b);
+    // sums behind the first request that fails are never used; they only need to stay in range
+    cu[b] = (int)min(ct, (long long)p.T);
+    pg[b] = (int)min(cp, (long long)n_free);
+    const bool valid = o >= 0 && n >= 0;
+    const long long pages = valid ? (o + n + p.ps - 1) / p.ps : 0;
+    if (valid) {
+      ct += n;
+      cp += pages - (o + p.ps - 1) / p.ps;
+    }
+    if ((!valid || pages > p.max_pages || ct > p.T || cp > n_free) && bad == p.B) bad = b;
+  }
+  if (tid == nt - 1) {
+    cu[p.B] = (int)min(ct, (long long)p.T);
+    pg[p.B] = (int)min(cp, (long long)n_free);
+  }
+  if (bad < p.B) atomicMin(&fail, bad);
+  __syncthreads();
+  const int served = fail;
+  const int n_tok = cu[served], n_new = pg[served];
+  if (blockIdx.x == 0) {
+    for (int b = tid; b <= p.B; b += nt) p.cu[b] = b < served ? cu[b] : n_tok;
+    for (int b = tid; b < p.B; b += nt) p.seq_lens[b] = __ldg(p.old_lens + b) + (b < served ? __ldg(p.new_lens + b) : 0);
+    if (tid == 0) {
+      *p.n_free_out = n_free - n_new;
+      *p.n_served = served;
+    }
+  }
+  const int gid = blockIdx.x * nt + tid, gn = gridDim.x * nt;
+  for (int i = gid; i < n_new; i += gn) {
+    const int b = plan_upper(pg, served, i);
+    const int held = (int)(((long long)__ldg(p.old_lens + b) + p.ps - 1) / p.ps);
+    p.table[b * p.tstride + held + i - pg[b]] = __ldg(p.free_pages + (n_free - 1 - i));
+  }
+  for (int t = gid; t < p.T; t += gn) {
+    long long slot = -1;
+    if (t < n_tok) {
+      const int b = plan_upper(cu, served, t);
+      const int o = __ldg(p.old_lens + b), pos = o + t - cu[b];
+      const int held = (int)(((long long)o + p.ps - 1) / p.ps), j = pos / p.ps;
+      // entries below `held` are read here and entries from `held` on written above: never the same one
+      const int id = j < held ? p.table[b * p.tstride + j] : __ldg(p.free_pages + (n_free - 1 - (pg[b] + j - held)));
+      if (id >= 0) slot = (long long)id * p.ps + (pos - j * p.ps);
+    }
+    p.slots[t] = slot;
+  }
+}
+
+cudaError_t launch_page_plan(const PagePlan& p, cudaStream_t st) {
+  const unsigned block = p.B > 512 ? 1024 : 256;
+  const size_t smem = (size_t)(p.B + 1) * 2 * sizeof(int);
+  cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int grid = min(148, max(1, (int)((p.T + (long long)block - 1) / block)));
+  page_plan_kernel<<<grid, block, smem, st>>>(p);
+  count_launch();
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// write
+// ---------------------------------------------------------------------------
+// e of the least 2^e, in [-60, 60], with a <= top * 2^e, from the bits of a = 1.m 2^E:
+// 448 = 1.75 * 2^8 and 127 = 1.984375 * 2^6 (a = 0 and subnormals: -60).
+__device__ __forceinline__ int k8_exp_for(float a, int fmt) {
+  const uint32_t u = __float_as_uint(a);
+  const int E = (int)(u >> 23) - 127;
+  const uint32_t m = u & 0x7fffffu;
+  const int e = fmt == kFmtE4M3 ? E - (m <= 0x600000u ? 8 : 7) : E - (m <= 0x7e0000u ? 6 : 5);
+  return min(max(e, -60), 60);
+}
+// e of the least power of two at or above a scale that is already there
+__device__ __forceinline__ int k8_exp_at_least(float a) {
+  if (!(a > 0.f)) return -60;
+  const uint32_t u = __float_as_uint(a);
+  const int e = (int)(u >> 23) - 127 + ((u & 0x7fffffu) ? 1 : 0);
+  return min(max(e, -60), 60);
+}
+__device__ __forceinline__ float k8_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+template <bool F16>
+__device__ __forceinline__ void k8_unpack8(const uint4& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (F16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    } else {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+// m new rows (x, `stride` apart) of one head to rows [off, off + m) of a page; 128
+// threads, which meet at named barrier `bar`.
+template <bool F16>
+__device__ __forceinline__ void k8_write_part(const char* x, long long stride, int m, int d, uint8_t* codes,
+                                              long long row_bytes, int off, float* scale, int fmt, int tid, int bar,
+                                              float* red) {
+  const int per = d >> 3, n8 = m * per;
+  float a = 0.f;
+  for (int i = tid; i < n8; i += 128) {
+    const int r = i / per, c = i - r * per;
+    float v[8];
+    k8_unpack8<F16>(__ldg(reinterpret_cast<const uint4*>(x + r * stride * 2 + c * 16)), v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float s = fabsf(v[j]);
+      a = fmaxf(a, s < INFINITY ? s : 0.f);  // infinities and NaN set no scale
+    }
+  }
+#pragma unroll
+  for (int s = 16; s; s >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, s));
+  if ((tid & 31) == 0) red[tid >> 5] = a;
+  const float before = off ? *scale : 0.f;
+  asm volatile("bar.sync %0, 128;\n" ::"r"(bar) : "memory");
+  a = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  int e = k8_exp_for(a, fmt);
+  if (off) e = max(e, k8_exp_at_least(before));
+  const float after = k8_pow2(e), inv = k8_pow2(-e);  // x * 2^-e is x / s exactly
+  if (off && before != after) {
+    // rows that were there before: their codes in the new scale
+    const float ratio = before / after;
+    const int p4 = d >> 2;
+    for (int i = tid; i < off * p4; i += 128) {
+      const int r = i / p4;
+      uint32_t* at = reinterpret_cast<uint32_t*>(codes + r * row_bytes + (i - r * p4) * 4);
+      const uint32_t w = *at;
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = k8_code((uint8_t)(w >> (8 * j)), fmt) * ratio;
+      *at = k8_round2(v[0], v[1], fmt) | (k8_round2(v[2], v[3], fmt) << 16);
+    }
+  }
+  for (int i = tid; i < n8; i += 128) {
+    const int r = i / per, c = i - r * per;
+    float v[8];
+    k8_unpack8<F16>(__ldg(reinterpret_cast<const uint4*>(x + r * stride * 2 + c * 16)), v);
+    uint2 o;
+    o.x = k8_round2(v[0] * inv, v[1] * inv, fmt) | (k8_round2(v[2] * inv, v[3] * inv, fmt) << 16);
+    o.y = k8_round2(v[4] * inv, v[5] * inv, fmt) | (k8_round2(v[6] * inv, v[7] * inv, fmt) << 16);
+    *reinterpret_cast<uint2*>(codes + (off + r) * row_bytes + c * 8) = o;
+  }
+  asm volatile("bar.sync %0, 128;\n" ::"r"(bar) : "memory");  // red[] and the old scale have been read
+  if (tid == 0) *scale = after;
+}
+
+// One CTA per (window of tokens, head): it takes the page runs that begin in its
+// window (a run is the new rows of one page; a page's runs never split over CTAs, so
+// scale and codes have one writer).  Threads 0-127 write K and 128-255 V.
+template <bool F16>
+__global__ void __launch_bounds__(256) kv8_write_kernel(K8Write a) {
+  __shared__ float red[2][4];
+  const K8Cache& c = a.c;
+  const int h = blockIdx.y, half = threadIdx.x >> 7, tid = threadIdx.x & 127;
+  int t = blockIdx.x * a.window;
+  const int t_end = min(t + a.window, c.T);
+  int b = k8_find(c, t);
+  K8Seq s = k8_seq(c, b);
+  while (t < t_end) {
+    while (t >= s.t0 + s.n) {  // behind this sequence (or behind an empty one)
+      if (++b >= c.B) return;
+      s = k8_seq(c, b);
+      if (s.t0 > t) t = s.t0;  // offsets that leave a gap: no sequence's tokens
+      if (t >= t_end) return;
+    }
+    const int i = t - s.t0;
+    if (i < 0) return;  // offsets out of order
+    const int pos = s.first + i;
+    if (pos < 0) {
+      t -= pos;
+      continue;
+    }
+    const int j = pos / c.ps, off = pos - j * c.ps, m = min(c.ps - off, s.n - i);
+    const bool starts = i == 0 || off == 0 || pos == 0;
+    if (starts) {
+      const int page = k8_page(c, b, pos);
+      if (page >= 0) {
+        const long long row = ((long long)page * c.ps * c.Hkv + h);
+        const int d = half ? c.dv : c.dqk;
+        const char* x = half ? static_cast<const char*>(a.v) + (t * a.vstride + (long long)h * d) * 2
+                             : static_cast<const char*>(a.k) + (t * a.kstride + (long long)h * d) * 2;
+        if (!half || !c.shared)
+          k8_write_part<F16>(x, half ? a.vstride : a.kstride, m, d, (half ? c.v : c.k) + row * d,
+                             (long long)c.Hkv * d, off, (half ? c.vs : c.ks) + (long long)page * c.Hkv + h, c.fmt, tid,
+                             1 + half, red[half]);
+      }
+    }
+    t += m;
+  }
+}
+
+cudaError_t launch_kv8_write(K8Write a, cudaStream_t st) {
+  if (a.c.T == 0 || a.c.B == 0) return cudaSuccess;
+  // about 16 CTAs per SM: a window of one token while the tokens are few (each may begin a page run)
+  const long long items = (long long)a.c.T * a.c.Hkv;
+  a.window = (int)((items + 148 * 16 - 1) / (148 * 16));
+  if (a.window < 1) a.window = 1;
+  const dim3 grid((unsigned)((a.c.T + a.window - 1) / a.window), (unsigned)a.c.Hkv);
+  const unsigned block = a.c.shared ? 128 : 256;
+  if (a.f16) kv8_write_kernel<true><<<grid, block, 0, st>>>(a);
+  else kv8_write_kernel<false><<<grid, block, 0, st>>>(a);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace sa
