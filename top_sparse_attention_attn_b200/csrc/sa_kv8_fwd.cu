@@ -12,6 +12,743 @@ bool k8_built(int dqk, int dv, bool shared) {
   return (dqk == 64 && dv == 64) || (dqk == 128 && dv == 128) || (dqk == 192 && dv == 128);
 }
 
+// ---------------------------------------------------------------------------
+// separate K and V, or any row of at most 192 columns: split over the rows
+// ---------------------------------------------------------------------------
+// Work.  A unit is up to 16 query rows of one KV head: the G heads of 16 / G tokens
+// of a sequence, or 16 of a token's heads where G > 16, or the heads of one token where
+// each token selects its own blocks.  A unit's rows are cut into chunks of 64, and the
+// chunks of all units lie on one line that is cut evenly over the CTAs, wherever a unit
+// begins or ends: ragged lengths balance by themselves.  A unit that lies inside one
+// CTA is finished there; the others leave (maximum, sum, O) of each part in the
+// workspace for k8_join_kernel.
+// A warp takes 16 rows of a chunk through a pipeline of its own (cp.async, no block
+// barrier), keeps its own running maximum, sum and O, and the four warps meet once per
+// unit.  Codes become halves in registers right before the MMA (exact): K straight from
+// 16-byte reads of its rows, with the head dimension permuted alike in Q; V through
+// transposed ldmatrix of byte pairs, two output columns per 16-bit element.
+// Scales.  Q is held as halves times a power of two per row (exact for bf16 but for
+// what lies 2^-30 below the row's largest).  V's scale goes into the exponent: with
+// w_j = s_j + log2 vs_j the products use p'_j = 2^(w_j - max w), and the sum gets
+// p'_j / vs_j.  So P needs one exponential, and its 11 bits sit where the products are
+// largest whatever the pages' scales are.  p' <= 2^15: the maximum is let grow by up to
+// 2^4 before O is rescaled, and is held at 2^11.
+constexpr int kK8Warps = 4;
+constexpr int kK8Chunk = 16 * kK8Warps;
+constexpr float kK8Grow = 4.f, kK8Top = 11.f;
+
+template <int DK, int DV, bool ROWS>
+struct K8Split {
+  static constexpr int kMeta = ROWS ? 192 : 16;  // scales and rows of a step
+  static constexpr int kStage = 16 * (DK + DV) + kMeta;
+  static constexpr int kStages = DK + DV <= 128 ? 6 : 4;
+  static constexpr int kWarpBytes = kStage * kStages;
+  static constexpr int kSmem = kWarpBytes * kK8Warps;
+  static constexpr int kOcc = DK + DV <= 128 ? 4 : (DK <= 128 ? 3 : 2);
+  static constexpr int kLd = DV + 16;  // O in shared memory: rows 16 banks apart
+  static_assert(16 * kLd * 4 + 128 <= kWarpBytes, "the warps' results must fit in their stages");
+};
+
+// 16-byte piece of a row after the swizzle: 8 rows' same piece, and two rows' four
+// neighbouring pieces, fall on different banks.
+template <int D>
+__device__ __forceinline__ int k8_piece(int r, int c) {
+  if (D == 128) return c ^ (((r & 1) << 2) | ((r >> 1) & 3));
+  if (D == 64) return c ^ ((r >> 1) & 3);
+  return c;
+}
+
+template <int FMT>
+__device__ __forceinline__ void k8_pair(uint32_t w, uint32_t& lo, uint32_t& hi) {  // bytes (0, 1) and (2, 3)
+  if (FMT == kFmtE4M3) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  } else {
+    // 1024 + (code + 128) as a half is the byte under 0x64; the subtraction is exact
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), off), y = __hsub2(*reinterpret_cast<__half2*>(&b), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+template <int FMT>
+__device__ __forceinline__ void k8_pair_t(uint32_t w, uint32_t& even, uint32_t& odd) {  // bytes (0, 2) and (1, 3)
+  if (FMT == kFmtE4M3) {
+    k8_pair<FMT>(__byte_perm(w, 0, 0x3120), even, odd);
+  } else {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4240), b = __byte_perm(u, 0x64646464u, 0x4341);
+    const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), off), y = __hsub2(*reinterpret_cast<__half2*>(&b), off);
+    even = *reinterpret_cast<const uint32_t*>(&x);
+    odd = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+__device__ __forceinline__ void k8_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void k8_cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void k8_cp_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float k8_log2(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Where a unit's parts go: output row r is token t + r / gdiv, head head + r % gdiv.
+struct K8Join {
+  long long begin, end;  // the unit on the line of chunks; begin < 0: nothing to join
+  long long line;        // length of the line
+  int n;                 // CTAs that share it
+  int t, head, rows, gdiv;
+};
+// The workspace: a K8Join per CTA (the unit that begins in it and ends in a later one),
+// then two parts per CTA: (maximum, sum) of 16 rows and O [16][DV].
+__host__ __device__ inline size_t k8_parts_at(int n_cta) { return ((size_t)n_cta * sizeof(K8Join) + 255) / 256 * 256; }
+__host__ __device__ inline size_t k8_part_floats(int dv) { return 32 + 16 * (size_t)dv; }
+
+// One output row's four columns from base (maximum - kK8Top), sum and O.
+__device__ __forceinline__ void k8_finish(const K8Fwd& a, int t, int head, int d, float m, float l, float4 o) {
+  float base = m == -INFINITY ? m : m - kK8Top;
+  if (a.sinks) {
+    const float sink = __ldg(a.sinks + head) * 1.4426950408889634f, top = fmaxf(base, sink);
+    if (top != -INFINITY) {
+      const float f = exp2f(base - top);
+      l = l * f + exp2f(sink - top);
+      o.x *= f; o.y *= f; o.z *= f; o.w *= f;
+      base = top;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const long long row = (long long)t * a.Hq + head;
+  uint2 out;
+  if (a.f16) {
+    const __half2 x = __floats2half2_rn(o.x * inv, o.y * inv), y = __floats2half2_rn(o.z * inv, o.w * inv);
+    out = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  } else {
+    out = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  }
+  *reinterpret_cast<uint2*>(static_cast<char*>(a.o) + (row * a.c.dv + d) * 2) = out;
+  if (d == 0) a.lse[row] = l == 0.f ? INFINITY : 0.6931471805599453f * (base + log2f(l));
+}
+
+struct K8Geom {
+  int tpt;     // tokens per unit
+  int hs;      // units over a token's heads
+  int gdiv;    // query rows of a token in a unit
+  int sel_ch;  // chunks of a unit that selects (0: every row)
+};
+__host__ __device__ inline K8Geom k8_geom(const K8Fwd& a) {
+  K8Geom g;
+  g.gdiv = a.G < 16 ? a.G : 16;
+  g.hs = (a.G + 15) / 16;
+  g.tpt = a.topk || a.G > 16 ? 1 : 16 / a.G;
+  g.sel_ch = a.topk ? (int)(((long long)a.topk * a.bs + kK8Chunk - 1) / kK8Chunk) : 0;
+  return g;
+}
+
+// units and chunks per unit of a sequence
+struct K8Span {
+  K8Seq s;
+  int units, ch;
+};
+__device__ __forceinline__ K8Span k8_span(const K8Fwd& a, const K8Geom& g, int b) {
+  K8Span r;
+  r.s = k8_seq(a.c, b);
+  r.units = (r.s.n + g.tpt - 1) / g.tpt * g.hs * a.c.Hkv;
+  if (g.sel_ch) {
+    r.ch = g.sel_ch;
+  } else {
+    r.ch = max((r.s.L + kK8Chunk - 1) / kK8Chunk, 1);
+    // a window: from the step of 16 that its first row lies in
+    if (a.win < (1 << 29)) r.ch = min(r.ch, (a.win + g.tpt + 15 + kK8Chunk - 1) / kK8Chunk);
+  }
+  return r;
+}
+
+__device__ __forceinline__ long long k8_block_sum(long long v, long long* red, int tid) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+  __syncthreads();
+  if ((tid & 31) == 0) red[tid >> 5] = v;
+  __syncthreads();
+  return red[0] + red[1] + red[2] + red[3];
+}
+
+template <int DK, int DV, bool ROWS, int FMT>
+__global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_kernel(const K8Fwd a, float* ws) {
+  using P = K8Split<DK, DV, ROWS>;
+  constexpr int S = P::kStages;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ long long red[4];
+  __shared__ long long found[2];  // sequence and where it begins on the line
+  const K8Cache& c = a.c;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, q4 = lane & 3;
+  const K8Geom geo = k8_geom(a);
+
+  // the line's length, and the sequence that this CTA's share begins in
+  long long mine = 0;
+  for (int b = tid; b < c.B; b += 128) {
+    const K8Span sp = k8_span(a, geo, b);
+    mine += (long long)sp.units * sp.ch;
+  }
+  const long long W = k8_block_sum(mine, red, tid);
+  const int n_cta = (int)min(W, (long long)gridDim.x);  // nobody's share is empty but theirs who return
+  const long long w0 = n_cta ? W * blockIdx.x / n_cta : 0, w1 = n_cta ? W * (blockIdx.x + 1) / n_cta : 0;
+  K8Join* joins = reinterpret_cast<K8Join*>(ws);
+  float* parts = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + k8_parts_at(gridDim.x)) +
+                 2 * blockIdx.x * k8_part_floats(DV);
+  if (tid == 0) joins[blockIdx.x].begin = -1;
+  if (blockIdx.x >= n_cta) return;
+  {
+    long long before = 0;
+    for (int b0 = 0; b0 < c.B; b0 += 128) {
+      const int b = b0 + tid;
+      long long n = 0;
+      if (b < c.B) {
+        const K8Span sp = k8_span(a, geo, b);
+        n = (long long)sp.units * sp.ch;
+      }
+      long long inc = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(~0u, inc, d);
+        if (lane >= d) inc += x;
+      }
+      __syncthreads();
+      if (lane == 31) red[warp] = inc;
+      __syncthreads();
+      long long at = before + inc - n;
+      for (int w = 0; w < warp; ++w) at += red[w];
+      if (n > 0 && at <= w0 && w0 < at + n) {
+        found[0] = b;
+        found[1] = at;
+      }
+      before += red[0] + red[1] + red[2] + red[3];
+      if (before > w0) break;
+    }
+    __syncthreads();
+  }
+  int b = (int)found[0];
+  long long seq_at = found[1];
+  K8Span sp = k8_span(a, geo, b);
+
+  const uint32_t sbase = smem_u32(smem) + warp * P::kWarpBytes;
+  uint8_t* const wsm = smem + warp * P::kWarpBytes;
+  const int krs = c.Hkv * DK, vrs = c.Hkv * DV;  // bytes from row to row of the cache
+
+  for (long long w = w0; w < w1;) {
+    while (w >= seq_at + (long long)sp.units * sp.ch) {  // the next sequence with work
+      seq_at += (long long)sp.units * sp.ch;
+      sp = k8_span(a, geo, ++b);
+    }
+    const long long off = w - seq_at;
+    const int unit = (int)(off / sp.ch), c0 = (int)(off - (long long)unit * sp.ch);
+    const int c1 = (int)min((long long)sp.ch, c0 + (w1 - w));
+    const long long unit_at = seq_at + (long long)unit * sp.ch;
+    // unit -> (head, tokens, part of the heads); a KV head's units lie together
+    const int per_h = sp.units / c.Hkv, h = unit / per_h, ut = unit - h * per_h;
+    const int tile = ut / geo.hs, hp = ut - tile * geo.hs;
+    const int t0 = sp.s.t0 + tile * geo.tpt, ntok = min(geo.tpt, sp.s.n - tile * geo.tpt);
+    const int head0 = h * a.G + hp * 16, rows = geo.hs > 1 ? min(16, a.G - hp * 16) : ntok * a.G;
+    const int ta0 = sp.s.first + tile * geo.tpt, ta1 = ta0 + ntok - 1;  // rows of the first and last token
+    const int lo_all = a.win >= ta0 ? 0 : ta0 - a.win, hi_all = min(ta1 + 1, sp.s.L);
+    const int lo_last = a.win >= ta1 ? 0 : ta1 - a.win;
+    const int start = lo_all & ~15;
+    const long long iu = (long long)t0 * c.Hkv + h;
+    const int* idx = a.topk ? a.idx + iu * a.topk : nullptr;
+    int slots = a.topk;
+    if (a.topk && a.topk_len) slots = min(slots, max(0, __ldg(a.topk_len + iu)));
+    const int* table = c.table + b * c.tstride;
+
+    // --- Q: this thread's rows gr and gr + 8, as halves times 2^(8 - E) ---------
+    uint32_t qa[DK / 16][4];
+    float fr[2];
+    int ta[2], lo[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = gr + 8 * r;
+      const int i = min(row / geo.gdiv, ntok - 1);
+      ta[r] = ta0 + i;
+      lo[r] = a.win >= ta[r] ? 0 : ta[r] - a.win;
+      const bool live = row < rows;
+      const char* src = static_cast<const char*>(a.q) +
+                        ((long long)(t0 + row / geo.gdiv) * a.qstride + (long long)(head0 + row % geo.gdiv) * DK) * 2;
+      uint4 raw[DK / 32];
+      float big = 0.f;
+#pragma unroll
+      for (int i4 = 0; i4 < DK / 32; ++i4) {
+        // columns 64 * (i4 / 2) + 16 * q4 + 8 * (i4 % 2) ..
+        raw[i4] = live ? __ldg(reinterpret_cast<const uint4*>(src + (64 * (i4 >> 1) + 16 * q4 + 8 * (i4 & 1)) * 2))
+                       : make_uint4(0, 0, 0, 0);
+        const uint32_t v[4] = {raw[i4].x, raw[i4].y, raw[i4].z, raw[i4].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = a.f16 ? __half22float2(*reinterpret_cast<const __half2*>(&v[j]))
+                                 : make_float2(__uint_as_float(v[j] << 16), __uint_as_float(v[j] & 0xffff0000u));
+          big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
+      const int E = big > 0.f ? max((int)(__float_as_uint(big) >> 23) - 127, -110) : 8;
+      const float mul = __uint_as_float((uint32_t)(8 - E + 127) << 23);
+      fr[r] = a.scale_log2 * __uint_as_float((uint32_t)(E - 8 + 127) << 23);
+#pragma unroll
+      for (int i4 = 0; i4 < DK / 32; ++i4) {
+        const uint32_t v[4] = {raw[i4].x, raw[i4].y, raw[i4].z, raw[i4].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = a.f16 ? __half22float2(*reinterpret_cast<const __half2*>(&v[j]))
+                                 : make_float2(__uint_as_float(v[j] << 16), __uint_as_float(v[j] & 0xffff0000u));
+          const __half2 hh = __floats2half2_rn(f.x * mul, f.y * mul);
+          // column 64 ch + 16 q4 + 4 s + {0, 1 | 2, 3} is k {2 q4, + 1 | + 8, + 9} of step 4 ch + s
+          const int col = 8 * (i4 & 1) + 2 * j, s = (i4 >> 1) * 4 + (col >> 2), up = (col >> 1) & 1;
+          qa[s][r + 2 * up] = *reinterpret_cast<const uint32_t*>(&hh);
+        }
+      }
+    }
+
+    // --- the steps of this warp: 16 rows of each chunk ----------------------------
+    const int n_steps = c1 - c0;
+    const int p0 = c0 * kK8Chunk + warp * 16 + (ROWS ? (lane & 15) : 0);
+    auto fetch_idx = [&](int k) -> int {
+      if (!a.topk) return 0;
+      const int slot = (p0 + k * kK8Chunk) / a.bs;
+      return k < n_steps && slot < slots ? __ldg(idx + slot) : -1;
+    };
+    auto resolve = [&](int k, int x) -> int {  // the (first) row of step k, -1: none
+      if (k >= n_steps) return -1;
+      const int p = p0 + k * kK8Chunk;
+      int row = start + p;
+      if (a.topk) {
+        if (x < 0) return -1;
+        if ((long long)x * a.bs >= sp.s.L) {
+          if (c.status) atomicOr(c.status, kStatusIndexRange);
+          return -1;
+        }
+        row = x * a.bs + p % a.bs;
+      }
+      const int last = ROWS ? row : row + 15;
+      return row < hi_all && last >= lo_all ? row : -1;
+    };
+    auto fetch_page = [&](int row) -> int { return row >= 0 ? __ldg(table + row / c.ps) : 0; };
+    auto issue = [&](int k, int row, int page) {
+      if (row >= 0 && (page < 0 || page >= c.n_pages)) {
+        if (c.status) atomicOr(c.status, kStatusIndexRange);
+        row = -1;
+      }
+      const int st = k % S;
+      const uint32_t dst = sbase + st * P::kStage, meta = dst + 16 * (DK + DV);
+      int* im = reinterpret_cast<int*>(wsm + st * P::kStage + 16 * (DK + DV));
+      const int rr = row >= 0 ? page * c.ps + row % c.ps : -1;  // row of the cache
+      if (ROWS) {
+        if (lane < 16) {
+          im[lane] = row;
+          if (row >= 0) {
+            k8_cp4(meta + 64 + 4 * lane, c.ks + (long long)page * c.Hkv + h);
+            k8_cp4(meta + 128 + 4 * lane, c.vs + (long long)page * c.Hkv + h);
+          }
+        }
+      } else {
+        if (lane == 2) im[2] = row;
+        if (row < 0) return;
+        if (lane == 0) k8_cp4(meta, c.ks + (long long)page * c.Hkv + h);
+        if (lane == 1) k8_cp4(meta + 4, c.vs + (long long)page * c.Hkv + h);
+      }
+#pragma unroll
+      for (int it = 0; it < DK / 32; ++it) {
+        const int i = it * 32 + lane, r = i / (DK / 16), pc = i - r * (DK / 16);
+        const int at = ROWS ? __shfl_sync(~0u, rr, r) : rr + r;
+        const bool ok = ROWS ? at >= 0 : row + r < hi_all && row + r >= lo_all;
+        cp_async16(dst + r * DK + k8_piece<DK>(r, pc) * 16, c.k + (long long)(ok ? at : 0) * krs + h * DK + pc * 16, ok);
+      }
+#pragma unroll
+      for (int it = 0; it < DV / 32; ++it) {
+        const int i = it * 32 + lane, r = i / (DV / 16), pc = i - r * (DV / 16);
+        const int at = ROWS ? __shfl_sync(~0u, rr, r) : rr + r;
+        const bool ok = ROWS ? at >= 0 : row + r < hi_all && row + r >= lo_all;
+        cp_async16(dst + 16 * DK + r * DV + k8_piece<DV>(r, pc) * 16,
+                   c.v + (long long)(ok ? at : 0) * vrs + h * DV + pc * 16, ok);
+      }
+    };
+
+    float o[DV / 16][2][4];
+#pragma unroll
+    for (int i = 0; i < DV / 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][e][j] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    int xs[S + 1], rw[S], pg[S];
+#pragma unroll
+    for (int k = 0; k <= S; ++k) xs[k] = fetch_idx(k);
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      rw[k] = resolve(k, xs[k]);
+      pg[k] = fetch_page(rw[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) {
+      issue(k, rw[k], pg[k]);
+      cp_async_commit();
+    }
+    int next_row = rw[S - 1], next_page = pg[S - 1], next_x = xs[S];
+
+    for (int k = 0; k < n_steps; ++k) {
+      k8_cp_wait<S - 2>();
+      __syncwarp();
+      issue(k + S - 1, next_row, next_page);
+      cp_async_commit();
+      next_row = resolve(k + S, next_x);
+      next_page = fetch_page(next_row);
+      next_x = fetch_idx(k + S + 1);
+
+      uint8_t* const st = wsm + (k % S) * P::kStage;
+      const uint32_t sk = sbase + (k % S) * P::kStage, sv = sk + 16 * DK;
+      const int* im = reinterpret_cast<const int*>(st + 16 * (DK + DV));
+      const int row0 = ROWS ? 0 : im[2];
+      if (!ROWS && row0 < 0) continue;
+      if (ROWS && __all_sync(~0u, im[lane & 15] < 0)) continue;
+
+      // scores of 16 rows
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int ch = 0; ch < DK / 64; ++ch)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = 8 * j + gr;
+          const uint4 kw = *reinterpret_cast<const uint4*>(st + r * DK + k8_piece<DK>(r, ch * 4 + q4) * 16);
+          const uint32_t v[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t b0, b1;
+            k8_pair<FMT>(v[e], b0, b1);
+            k8_mma(s[j], qa[ch * 4 + e], b0, b1);
+          }
+        }
+
+      // w = score + log2 of V's scale; what a row does not see becomes -inf
+      float iv[2][2];
+      bool full = false;
+      if (!ROWS) {
+        const float ks = k8_scale(__int_as_float(im[0])), vs = k8_scale(__int_as_float(im[1]));
+        const float f0 = fr[0] * ks, f1 = fr[1] * ks, lv = k8_log2(vs);
+        iv[0][0] = 1.f / vs;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          s[j][0] = fmaf(s[j][0], f0, lv);
+          s[j][1] = fmaf(s[j][1], f0, lv);
+          s[j][2] = fmaf(s[j][2], f1, lv);
+          s[j][3] = fmaf(s[j][3], f1, lv);
+        }
+        full = row0 + 15 <= ta0 && row0 >= lo_last;
+        if (!full) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int pos = row0 + 8 * j + 2 * q4 + (e & 1);
+              if (pos > ta[e >> 1] || pos < lo[e >> 1]) s[j][e] = -INFINITY;
+            }
+        }
+      } else {
+        const float* fm = reinterpret_cast<const float*>(im);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int col = 8 * j + 2 * q4 + e, pos = im[col];
+            const float ks = k8_scale(fm[16 + col]), vs = k8_scale(fm[32 + col]), lv = k8_log2(vs);
+            iv[j][e] = 1.f / vs;
+            s[j][e] = pos >= 0 && pos <= ta[0] && pos >= lo[0] ? fmaf(s[j][e], fr[0] * ks, lv) : -INFINITY;
+            s[j][e + 2] = pos >= 0 && pos <= ta[1] && pos >= lo[1] ? fmaf(s[j][e + 2], fr[1] * ks, lv) : -INFINITY;
+          }
+      }
+      if (FMT == kFmtE4M3 && !full && ntok > 1) {
+        // A NaN in a V row that some of the unit's tokens see and others do not: the
+        // product would carry it (0 * NaN) to all of them.  It is set into the rows that
+        // see it here, and out of the tile.
+        bool nan = false;
+        for (int i = lane; i < 4 * DV; i += 32) {
+          const uint32_t v = reinterpret_cast<const uint32_t*>(st + 16 * DK)[i];
+          nan = nan || __vcmpeq4(v & 0x7f7f7f7fu, 0x7f7f7f7fu);
+        }
+        if (__any_sync(~0u, nan)) {
+          for (int r = 0; r < 16; ++r) {
+            const int pos = ROWS ? im[r] : row0 + r;
+            const bool see[2] = {pos >= 0 && pos <= ta[0] && pos >= lo[0], pos >= 0 && pos <= ta[1] && pos >= lo[1]};
+#pragma unroll
+            for (int pc = 0; pc < DV / 16; ++pc) {
+              const uint32_t v =
+                  *reinterpret_cast<const uint32_t*>(st + 16 * DK + r * DV + k8_piece<DV>(r, pc) * 16 + 4 * q4);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                if (((v >> (8 * x)) & 0x7f) != 0x7f) continue;
+                if (see[0]) o[pc][x & 1][x >> 1] = __int_as_float(0x7fffffff);
+                if (see[1]) o[pc][x & 1][2 + (x >> 1)] = __int_as_float(0x7fffffff);
+              }
+            }
+          }
+          __syncwarp();
+          for (int i = lane; i < 4 * DV; i += 32) {
+            uint32_t* v = reinterpret_cast<uint32_t*>(st + 16 * DK) + i;
+            *v &= ~__vcmpeq4(*v & 0x7f7f7f7fu, 0x7f7f7f7fu);
+          }
+          __syncwarp();
+        }
+      }
+
+      // the running maximum; O is rescaled only when it grew by more than 2^kK8Grow
+      float mx[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 2));
+      }
+      if (__any_sync(~0u, mx[0] > m[0] + kK8Grow || mx[1] > m[1] + kK8Grow)) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float mn = fmaxf(m[r], mx[r]), al = mn == -INFINITY ? 1.f : ex2_approx(m[r] - mn);
+          m[r] = mn;
+          l[r] *= al;
+#pragma unroll
+          for (int i = 0; i < DV / 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              o[i][e][2 * r] *= al;
+              o[i][e][2 * r + 1] *= al;
+            }
+        }
+      }
+      uint32_t pa[4];
+      {
+        const float base0 = m[0] == -INFINITY ? 0.f : m[0] - kK8Top, base1 = m[1] == -INFINITY ? 0.f : m[1] - kK8Top;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          s[j][0] = ex2_approx(s[j][0] - base0);
+          s[j][1] = ex2_approx(s[j][1] - base0);
+          s[j][2] = ex2_approx(s[j][2] - base1);
+          s[j][3] = ex2_approx(s[j][3] - base1);
+          const __half2 x = __floats2half2_rn(s[j][0], s[j][1]), y = __floats2half2_rn(s[j][2], s[j][3]);
+          pa[2 * j] = *reinterpret_cast<const uint32_t*>(&x);
+          pa[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        if (!ROWS) {
+          l[0] = fmaf((s[0][0] + s[0][1]) + (s[1][0] + s[1][1]), iv[0][0], l[0]);
+          l[1] = fmaf((s[0][2] + s[0][3]) + (s[1][2] + s[1][3]), iv[0][0], l[1]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              l[0] = fmaf(s[j][e], iv[j][e], l[0]);
+              l[1] = fmaf(s[j][e + 2], iv[j][e], l[1]);
+            }
+        }
+      }
+      // O += P V: two pieces of 16 columns at a time
+#pragma unroll
+      for (int pc = 0; pc < DV / 16; pc += 2) {
+        uint32_t v[4];
+        const int r = (lane & 7) + (lane & 8), p = pc + (lane >> 4);
+        ldsm_x4_t(v, sv + r * DV + k8_piece<DV>(r, p) * 16);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t e0, o0, e1, o1;
+          k8_pair_t<FMT>(v[2 * x], e0, o0);
+          k8_pair_t<FMT>(v[2 * x + 1], e1, o1);
+          k8_mma(o[pc + x][0], pa, e0, e1);
+          k8_mma(o[pc + x][1], pa, o0, o1);
+        }
+      }
+    }
+    k8_cp_wait<0>();
+    __syncwarp();
+
+    // --- the warps' results meet: maximum, sum, O --------------------------------
+    float* fo = reinterpret_cast<float*>(wsm);
+    float* fm = fo + 16 * P::kLd;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(~0u, l[r], 1);
+      l[r] += __shfl_xor_sync(~0u, l[r], 2);
+      if (q4 == 0) {
+        fm[gr + 8 * r] = m[r];
+        fm[16 + gr + 8 * r] = l[r];
+      }
+#pragma unroll
+      for (int i = 0; i < DV / 16; ++i)
+        *reinterpret_cast<float4*>(fo + (gr + 8 * r) * P::kLd + 16 * i + 4 * q4) =
+            make_float4(o[i][0][2 * r], o[i][1][2 * r], o[i][0][2 * r + 1], o[i][1][2 * r + 1]);
+    }
+    __syncthreads();
+    {
+      const int row = tid >> 3, part = tid & 7;
+      const float* f0 = reinterpret_cast<const float*>(smem);
+      constexpr int kW = P::kWarpBytes / 4;
+      float mw[kK8Warps], top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int x = 0; x < kK8Warps; ++x) {
+        mw[x] = f0[x * kW + 16 * P::kLd + row];
+        top = fmaxf(top, mw[x]);
+      }
+#pragma unroll
+      for (int x = 0; x < kK8Warps; ++x) {
+        mw[x] = top == -INFINITY ? 1.f : ex2_approx(mw[x] - top);
+        sum = fmaf(f0[x * kW + 16 * P::kLd + 16 + row], mw[x], sum);
+      }
+      const bool whole = c0 == 0 && c1 == sp.ch;
+      // a part of a unit: slot 0 holds the one that this CTA's share begins with
+      float* part_out = parts + (w == w0 ? 0 : k8_part_floats(DV));
+      if (row < rows) {
+        const int t = t0 + row / geo.gdiv, head = head0 + row % geo.gdiv;
+#pragma unroll
+        for (int i = 0; i < DV / 32; ++i) {
+          const int d = 4 * (part + 8 * i);
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int x = 0; x < kK8Warps; ++x) {
+            const float4 y = *reinterpret_cast<const float4*>(f0 + x * kW + row * P::kLd + d);
+            v.x = fmaf(y.x, mw[x], v.x);
+            v.y = fmaf(y.y, mw[x], v.y);
+            v.z = fmaf(y.z, mw[x], v.z);
+            v.w = fmaf(y.w, mw[x], v.w);
+          }
+          if (whole) k8_finish(a, t, head, d, top, sum, v);
+          else *reinterpret_cast<float4*>(part_out + 32 + row * DV + d) = v;
+        }
+        if (!whole && part == 0) {
+          part_out[row] = top;
+          part_out[16 + row] = sum;
+        }
+      }
+      if (!whole && c0 == 0 && tid == 0) {
+        K8Join jn;
+        jn.begin = unit_at;
+        jn.end = unit_at + sp.ch;
+        jn.line = W;
+        jn.n = n_cta;
+        jn.t = t0;
+        jn.head = head0;
+        jn.rows = rows;
+        jn.gdiv = geo.gdiv;
+        joins[blockIdx.x] = jn;
+      }
+    }
+    __syncthreads();  // the stages are filled again
+    w += c1 - c0;
+  }
+}
+
+// The units that span several CTAs: blocks 4 i .. 4 i + 3 join the rows of the unit that
+// begins in CTA i's share and ends behind it.  Its part in CTA x lies in slot 0 where the
+// share of x begins inside the unit (or with it), else in slot 1.  A row takes four
+// warps, each over a quarter of the parts, in a fixed order.
+template <int DV>
+__global__ void __launch_bounds__(512) k8_join_kernel(const K8Fwd a, const float* ws, int n_grid) {
+  __shared__ float sl[16];
+  __shared__ float4 so[16][DV / 4];
+  pdl_wait();
+  const int i = blockIdx.x >> 2, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const K8Join jn = reinterpret_cast<const K8Join*>(ws)[i];
+  if (jn.begin < 0) return;
+  const int row = (blockIdx.x & 3) * 4 + (warp >> 2);
+  const float* parts = reinterpret_cast<const float*>(reinterpret_cast<const char*>(ws) + k8_parts_at(n_grid));
+  const int first = 2 * i + (jn.line * i / jn.n == jn.begin ? 0 : 1);
+  const int n = (int)((jn.end * jn.n + jn.line - 1) / jn.line) - i;  // parts: of CTAs i .. i + n - 1
+  auto part = [&](int x) { return parts + (x ? 2 * (i + x) : first) * k8_part_floats(DV); };
+  const bool live = row < jn.rows;
+  float top = -INFINITY, sum = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (live) {
+    for (int x = lane; x < n; x += 32) top = fmaxf(top, part(x)[row]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+#pragma unroll 4
+    for (int x = warp & 3; x < n; x += 4) {
+      const float* p = part(x);
+      const float f = top == -INFINITY ? 1.f : ex2_approx(p[row] - top);
+      sum = fmaf(p[16 + row], f, sum);
+      if (lane < DV / 4) {
+        const float4 y = *reinterpret_cast<const float4*>(p + 32 + row * DV + 4 * lane);
+        v.x = fmaf(y.x, f, v.x);
+        v.y = fmaf(y.y, f, v.y);
+        v.z = fmaf(y.z, f, v.z);
+        v.w = fmaf(y.w, f, v.w);
+      }
+    }
+    if (lane == 0) sl[warp] = sum;
+    if (lane < DV / 4) so[warp][lane] = v;
+  }
+  __syncthreads();
+  if (!live || (warp & 3) || lane >= DV / 4) return;
+  sum = 0.f;
+  v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    sum += sl[warp + x];
+    const float4 y = so[warp + x][lane];
+    v.x += y.x;
+    v.y += y.y;
+    v.z += y.z;
+    v.w += y.w;
+  }
+  k8_finish(a, jn.t + row / jn.gdiv, jn.head + row % jn.gdiv, 4 * lane, top, sum, v);
+}
+
+// CTAs of the split kernel: all that the SMs hold at once, or as many as the longest
+// possible line has chunks.
+static int k8_split_ctas(const K8Fwd& a) {
+  const K8Geom g = k8_geom(a);
+  const int occ = a.c.dqk + a.c.dv <= 128 ? 4 : (a.c.dqk <= 128 ? 3 : 2);
+  const long long units = ((long long)(a.c.T + g.tpt - 1) / g.tpt + (g.tpt > 1 ? min(a.c.B, a.c.T) : 0)) * g.hs * a.c.Hkv;
+  long long ch = g.sel_ch;
+  if (!ch) {
+    ch = ((long long)a.c.max_pages * a.c.ps + kK8Chunk - 1) / kK8Chunk;
+    if (a.win < (1 << 29)) ch = min(ch, (long long)(a.win + g.tpt + 15 + kK8Chunk - 1) / kK8Chunk);
+  }
+  return (int)min((long long)148 * occ, units * max(ch, 1ll));
+}
+
+template <int DK, int DV, bool ROWS, int FMT>
+static cudaError_t split_t(const K8Fwd& a, void* ws, cudaStream_t st) {
+  using P = K8Split<DK, DV, ROWS>;
+  auto k = k8_split_kernel<DK, DV, ROWS, FMT>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  if (e != cudaSuccess) return e;
+  const int n = k8_split_ctas(a);
+  k<<<(unsigned)n, 128, P::kSmem, st>>>(a, static_cast<float*>(ws));
+  count_launch();
+  e = cudaGetLastError();
+  if (e != cudaSuccess || n == 1) return e;
+  count_launch();
+  return launch_pdl(k8_join_kernel<DV>, 4u * n, 512, 0, st, a, (const float*)ws, n);
+}
+
+template <int DK, int DV>
+static cudaError_t split_d(const K8Fwd& a, void* ws, cudaStream_t st) {
+  // steps of 16 rows lie in one page, and in one block, unless these sizes break them
+  const bool rows = a.c.ps % 16 != 0 || (a.topk && a.bs % 16 != 0);
+  if (a.c.fmt == kFmtE4M3)
+    return rows ? split_t<DK, DV, true, kFmtE4M3>(a, ws, st) : split_t<DK, DV, false, kFmtE4M3>(a, ws, st);
+  return rows ? split_t<DK, DV, true, kFmtInt8>(a, ws, st) : split_t<DK, DV, false, kFmtInt8>(a, ws, st);
+}
+
 // One CTA per (token, query head): scores of 128 rows at a time, one per thread,
 // an online softmax, then each thread sums its output columns over the rows.
 __global__ void __launch_bounds__(128) k8_row_kernel(K8Fwd a) {
@@ -102,13 +839,24 @@ __global__ void __launch_bounds__(128) k8_row_kernel(K8Fwd a) {
   if (tid == 0) a.lse[(long long)t * a.Hq + hq] = l == 0.f ? INFINITY : 0.6931471805599453f * (m + log2f(l));
 }
 
-size_t k8_fwd_workspace(const K8Fwd&) { return 0; }
+static bool k8_latent(const K8Fwd& a) { return a.c.dqk > 192; }
 
-cudaError_t launch_kv8_fwd(const K8Fwd& a, void*, cudaStream_t st) {
+size_t k8_fwd_workspace(const K8Fwd& a) {
+  if (k8_latent(a)) return 0;
+  const int n = k8_split_ctas(a);
+  return k8_parts_at(n) + (size_t)n * 2 * k8_part_floats(a.c.dv) * sizeof(float);
+}
+
+cudaError_t launch_kv8_fwd(const K8Fwd& a, void* ws, cudaStream_t st) {
   if (a.c.T == 0 || a.c.B == 0) return cudaSuccess;
-  k8_row_kernel<<<dim3((unsigned)a.c.T, (unsigned)a.Hq), 128, 0, st>>>(a);
-  count_launch();
-  return cudaGetLastError();
+  if (k8_latent(a)) {
+    k8_row_kernel<<<dim3((unsigned)a.c.T, (unsigned)a.Hq), 128, 0, st>>>(a);
+    count_launch();
+    return cudaGetLastError();
+  }
+  if (a.c.dqk == 64) return split_d<64, 64>(a, ws, st);
+  if (a.c.dqk == 128) return split_d<128, 128>(a, ws, st);
+  return split_d<192, 128>(a, ws, st);
 }
 
 }  // namespace sa
