@@ -11,9 +11,25 @@ namespace sa {
 enum { kFmtE4M3 = 0, kFmtInt8 = 1 };
 constexpr int kPlanMaxBatch = 24576;  // two prefix arrays of 4 bytes in shared memory
 
+// n / d for 0 <= n < 2^31 by a multiplication: with 2^s >= d and m = ceil(2^(31+s) / d),
+// m d exceeds 2^(31+s) by less than 2^s, so n m / 2^(31+s) exceeds n / d by less than 1 / d.
+struct K8Div {
+  uint32_t m;
+  int s, d;
+};
+inline K8Div k8_div_of(int d) {
+  K8Div r;
+  r.d = d;
+  r.s = 0;
+  while ((1ll << r.s) < d) ++r.s;
+  r.m = (uint32_t)(((1ull << (31 + r.s)) + d - 1) / d);
+  return r;
+}
+
 // The cache and the step's tokens (see sa_kv8_cache).
 struct K8Cache {
   int fmt, Hkv, dqk, dv, shared, ps, n_pages, B, max_pages;
+  K8Div by_ps;
   int s_q;  // tokens per sequence when cu is null
   int T;    // rows of the packed token axis
   long long tstride;
@@ -34,6 +50,7 @@ struct K8Write {
 struct K8Fwd {
   K8Cache c;
   int f16, Hq, G, bs, topk;
+  K8Div by_bs;
   int win;           // rows before the token's own that it sees (INT_MAX: all)
   float scale_log2;  // scale * log2(e)
   const void* q;

@@ -53,6 +53,7 @@ sa::K8Cache make_cache(const sa_kv8_cache* c) {
   r.dv = c->d_v;
   r.shared = c->kv_shared ? 1 : 0;
   r.ps = c->page_size;
+  r.by_ps = sa::k8_div_of(c->page_size);
   r.n_pages = c->n_pages;
   r.B = c->batch;
   r.max_pages = c->max_pages;
@@ -96,6 +97,7 @@ sa::K8Fwd make_fwd(const sa_kv8_cache* c, const sa_kv8_query* q) {
   r.Hq = q->n_heads_q;
   r.G = q->n_heads_q / c->n_heads_kv;
   r.bs = q->block_size;
+  r.by_bs = sa::k8_div_of(q->block_size);
   r.topk = q->topk;
   r.win = q->win_left < 0 || q->win_left > INT_MAX ? INT_MAX : (int)q->win_left;
   r.scale_log2 = q->scale * 1.4426950408889634f;

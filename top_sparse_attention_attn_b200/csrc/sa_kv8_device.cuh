@@ -11,6 +11,9 @@
 
 namespace sa {
 
+__device__ __forceinline__ int k8_quot(const K8Div& v, int n) { return (int)(__umulhi(2u * (uint32_t)n, v.m) >> v.s); }
+__device__ __forceinline__ int k8_rem(const K8Div& v, int n) { return n - k8_quot(v, n) * v.d; }
+
 // Scales as the kernels use them: [2^-60, 2^60], NaN as 2^-60 (fmaxf drops it).
 __device__ __forceinline__ float k8_scale(float s) { return fminf(fmaxf(s, 0x1p-60f), 0x1p60f); }
 

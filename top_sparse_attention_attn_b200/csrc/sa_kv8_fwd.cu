@@ -100,10 +100,35 @@ template <int N>
 __device__ __forceinline__ void k8_cp_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ float k8_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ float k8_log2(float x) {
   float r;
   asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
   return r;
+}
+
+// 16 rows of D bytes, `rs` bytes apart, to shared memory; with EDGE, rows outside [lo, hi) are zeros.
+template <int D, bool EDGE>
+__device__ __forceinline__ void k8_copy_step(uint32_t dst, const uint8_t* src, int rs, int lane, int lo, int hi) {
+#pragma unroll
+  for (int it = 0; it < D / 32; ++it) {
+    const int i = it * 32 + lane, r = i / (D / 16), pc = i - r * (D / 16);
+    cp_async16(dst + r * D + k8_piece<D>(r, pc) * 16, src + r * rs + pc * 16, !EDGE || (r >= lo && r < hi));
+  }
+}
+// 16 rows of which lane r holds the row of the cache (negative: zeros)
+template <int D>
+__device__ __forceinline__ void k8_copy_rows(uint32_t dst, const uint8_t* src, int rs, int rr, int lane) {
+#pragma unroll
+  for (int it = 0; it < D / 32; ++it) {
+    const int i = it * 32 + lane, r = i / (D / 16), pc = i - r * (D / 16);
+    const int at = __shfl_sync(~0u, rr, r);
+    cp_async16(dst + r * D + k8_piece<D>(r, pc) * 16, src + (long long)(at >= 0 ? at : 0) * rs + pc * 16, at >= 0);
+  }
 }
 
 // Where a unit's parts go: output row r is token t + r / gdiv, head head + r % gdiv.
@@ -325,7 +350,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
     const int p0 = c0 * kK8Chunk + warp * 16 + (ROWS ? (lane & 15) : 0);
     auto fetch_idx = [&](int k) -> int {
       if (!a.topk) return 0;
-      const int slot = (p0 + k * kK8Chunk) / a.bs;
+      const int slot = k8_quot(a.by_bs, p0 + k * kK8Chunk);
       return k < n_steps && slot < slots ? __ldg(idx + slot) : -1;
     };
     auto resolve = [&](int k, int x) -> int {  // the (first) row of step k, -1: none
@@ -338,21 +363,20 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
           if (c.status) atomicOr(c.status, kStatusIndexRange);
           return -1;
         }
-        row = x * a.bs + p % a.bs;
+        row = x * a.bs + k8_rem(a.by_bs, p);
       }
       const int last = ROWS ? row : row + 15;
       return row < hi_all && last >= lo_all ? row : -1;
     };
-    auto fetch_page = [&](int row) -> int { return row >= 0 ? __ldg(table + row / c.ps) : 0; };
-    auto issue = [&](int k, int row, int page) {
+    auto fetch_page = [&](int row) -> int { return row >= 0 ? __ldg(table + k8_quot(c.by_ps, row)) : 0; };
+    auto issue = [&](int st, int row, int page) {
       if (row >= 0 && (page < 0 || page >= c.n_pages)) {
         if (c.status) atomicOr(c.status, kStatusIndexRange);
         row = -1;
       }
-      const int st = k % S;
       const uint32_t dst = sbase + st * P::kStage, meta = dst + 16 * (DK + DV);
       int* im = reinterpret_cast<int*>(wsm + st * P::kStage + 16 * (DK + DV));
-      const int rr = row >= 0 ? page * c.ps + row % c.ps : -1;  // row of the cache
+      const int rr = row >= 0 ? page * c.ps + k8_rem(c.by_ps, row) : -1;  // row of the cache
       if (ROWS) {
         if (lane < 16) {
           im[lane] = row;
@@ -367,20 +391,19 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
         if (lane == 0) k8_cp4(meta, c.ks + (long long)page * c.Hkv + h);
         if (lane == 1) k8_cp4(meta + 4, c.vs + (long long)page * c.Hkv + h);
       }
-#pragma unroll
-      for (int it = 0; it < DK / 32; ++it) {
-        const int i = it * 32 + lane, r = i / (DK / 16), pc = i - r * (DK / 16);
-        const int at = ROWS ? __shfl_sync(~0u, rr, r) : rr + r;
-        const bool ok = ROWS ? at >= 0 : row + r < hi_all && row + r >= lo_all;
-        cp_async16(dst + r * DK + k8_piece<DK>(r, pc) * 16, c.k + (long long)(ok ? at : 0) * krs + h * DK + pc * 16, ok);
-      }
-#pragma unroll
-      for (int it = 0; it < DV / 32; ++it) {
-        const int i = it * 32 + lane, r = i / (DV / 16), pc = i - r * (DV / 16);
-        const int at = ROWS ? __shfl_sync(~0u, rr, r) : rr + r;
-        const bool ok = ROWS ? at >= 0 : row + r < hi_all && row + r >= lo_all;
-        cp_async16(dst + 16 * DK + r * DV + k8_piece<DV>(r, pc) * 16,
-                   c.v + (long long)(ok ? at : 0) * vrs + h * DV + pc * 16, ok);
+      if (ROWS) {
+        k8_copy_rows<DK>(dst, c.k + h * DK, krs, rr, lane);
+        k8_copy_rows<DV>(dst + 16 * DK, c.v + h * DV, vrs, rr, lane);
+      } else {
+        const uint8_t* ksrc = c.k + (long long)rr * krs + h * DK;
+        const uint8_t* vsrc = c.v + (long long)rr * vrs + h * DV;
+        if (row >= lo_all && row + 16 <= hi_all) {
+          k8_copy_step<DK, false>(dst, ksrc, krs, lane, 0, 16);
+          k8_copy_step<DV, false>(dst + 16 * DK, vsrc, vrs, lane, 0, 16);
+        } else {  // zeros in the rows that none of the unit's tokens sees
+          k8_copy_step<DK, true>(dst, ksrc, krs, lane, lo_all - row, hi_all - row);
+          k8_copy_step<DV, true>(dst + 16 * DK, vsrc, vrs, lane, lo_all - row, hi_all - row);
+        }
       }
     };
 
@@ -392,6 +415,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][e][j] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float base[2] = {0.f, 0.f}, limit[2] = {-INFINITY, -INFINITY};  // m - kK8Top, and how far above it w may lie
 
     int xs[S + 1], rw[S], pg[S];
 #pragma unroll
@@ -408,17 +432,20 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
     }
     int next_row = rw[S - 1], next_page = pg[S - 1], next_x = xs[S];
 
+    int at = 0, fill = S - 1;  // stages of step k and of the one that is fetched
     for (int k = 0; k < n_steps; ++k) {
       k8_cp_wait<S - 2>();
       __syncwarp();
-      issue(k + S - 1, next_row, next_page);
+      issue(fill, next_row, next_page);
       cp_async_commit();
       next_row = resolve(k + S, next_x);
       next_page = fetch_page(next_row);
       next_x = fetch_idx(k + S + 1);
 
-      uint8_t* const st = wsm + (k % S) * P::kStage;
-      const uint32_t sk = sbase + (k % S) * P::kStage, sv = sk + 16 * DK;
+      uint8_t* const st = wsm + at * P::kStage;
+      const uint32_t sv = sbase + at * P::kStage + 16 * DK;
+      fill = at;
+      at = at + 1 == S ? 0 : at + 1;
       const int* im = reinterpret_cast<const int*>(st + 16 * (DK + DV));
       const int row0 = ROWS ? 0 : im[2];
       if (!ROWS && row0 < 0) continue;
@@ -441,19 +468,20 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
           }
         }
 
-      // w = score + log2 of V's scale; what a row does not see becomes -inf
+      // w = score + log2 of V's scale, less what the exponential's argument starts from;
+      // what a row does not see becomes -inf
       float iv[2][2];
       bool full = false;
       if (!ROWS) {
         const float ks = k8_scale(__int_as_float(im[0])), vs = k8_scale(__int_as_float(im[1]));
-        const float f0 = fr[0] * ks, f1 = fr[1] * ks, lv = k8_log2(vs);
-        iv[0][0] = 1.f / vs;
+        const float f0 = fr[0] * ks, f1 = fr[1] * ks, lv = k8_log2(vs), a0 = lv - base[0], a1 = lv - base[1];
+        iv[0][0] = k8_rcp(vs);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          s[j][0] = fmaf(s[j][0], f0, lv);
-          s[j][1] = fmaf(s[j][1], f0, lv);
-          s[j][2] = fmaf(s[j][2], f1, lv);
-          s[j][3] = fmaf(s[j][3], f1, lv);
+          s[j][0] = fmaf(s[j][0], f0, a0);
+          s[j][1] = fmaf(s[j][1], f0, a0);
+          s[j][2] = fmaf(s[j][2], f1, a1);
+          s[j][3] = fmaf(s[j][3], f1, a1);
         }
         full = row0 + 15 <= ta0 && row0 >= lo_last;
         if (!full) {
@@ -473,9 +501,10 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
           for (int e = 0; e < 2; ++e) {
             const int col = 8 * j + 2 * q4 + e, pos = im[col];
             const float ks = k8_scale(fm[16 + col]), vs = k8_scale(fm[32 + col]), lv = k8_log2(vs);
-            iv[j][e] = 1.f / vs;
-            s[j][e] = pos >= 0 && pos <= ta[0] && pos >= lo[0] ? fmaf(s[j][e], fr[0] * ks, lv) : -INFINITY;
-            s[j][e + 2] = pos >= 0 && pos <= ta[1] && pos >= lo[1] ? fmaf(s[j][e + 2], fr[1] * ks, lv) : -INFINITY;
+            iv[j][e] = k8_rcp(vs);
+            s[j][e] = pos >= 0 && pos <= ta[0] && pos >= lo[0] ? fmaf(s[j][e], fr[0] * ks, lv - base[0]) : -INFINITY;
+            s[j][e + 2] =
+                pos >= 0 && pos <= ta[1] && pos >= lo[1] ? fmaf(s[j][e + 2], fr[1] * ks, lv - base[1]) : -INFINITY;
           }
       }
       if (FMT == kFmtE4M3 && !full && ntok > 1) {
@@ -515,16 +544,23 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
       // the running maximum; O is rescaled only when it grew by more than 2^kK8Grow
       float mx[2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < 2; ++r)
         mx[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 2));
-      }
-      if (__any_sync(~0u, mx[0] > m[0] + kK8Grow || mx[1] > m[1] + kK8Grow)) {
+      if (__any_sync(~0u, mx[0] > limit[0] || mx[1] > limit[1])) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float mn = fmaxf(m[r], mx[r]), al = mn == -INFINITY ? 1.f : ex2_approx(m[r] - mn);
+          mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 1));
+          mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 2));
+          const float mn = fmaxf(m[r], mx[r] + base[r]);
+          if (mn == -INFINITY) continue;
+          const float al = ex2_approx(m[r] - mn), shift = base[r] - (mn - kK8Top);
           m[r] = mn;
+          base[r] = mn - kK8Top;
+          limit[r] = kK8Top + kK8Grow;
+          s[0][2 * r] += shift;
+          s[0][2 * r + 1] += shift;
+          s[1][2 * r] += shift;
+          s[1][2 * r + 1] += shift;
           l[r] *= al;
 #pragma unroll
           for (int i = 0; i < DV / 16; ++i)
@@ -537,13 +573,12 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
       }
       uint32_t pa[4];
       {
-        const float base0 = m[0] == -INFINITY ? 0.f : m[0] - kK8Top, base1 = m[1] == -INFINITY ? 0.f : m[1] - kK8Top;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          s[j][0] = ex2_approx(s[j][0] - base0);
-          s[j][1] = ex2_approx(s[j][1] - base0);
-          s[j][2] = ex2_approx(s[j][2] - base1);
-          s[j][3] = ex2_approx(s[j][3] - base1);
+          s[j][0] = ex2_approx(s[j][0]);
+          s[j][1] = ex2_approx(s[j][1]);
+          s[j][2] = ex2_approx(s[j][2]);
+          s[j][3] = ex2_approx(s[j][3]);
           const __half2 x = __floats2half2_rn(s[j][0], s[j][1]), y = __floats2half2_rn(s[j][2], s[j][3]);
           pa[2 * j] = *reinterpret_cast<const uint32_t*>(&x);
           pa[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&y);
