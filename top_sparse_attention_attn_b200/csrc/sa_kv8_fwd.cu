@@ -58,6 +58,10 @@ __device__ __forceinline__ int k8_piece(int r, int c) {
   return c;
 }
 
+__device__ __forceinline__ float2 k8_two(uint32_t v, int f16) {
+  return f16 ? __half22float2(*reinterpret_cast<const __half2*>(&v))
+             : make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
 template <int FMT>
 __device__ __forceinline__ void k8_pair(uint32_t w, uint32_t& lo, uint32_t& hi) {  // bytes (0, 1) and (2, 3)
   if (FMT == kFmtE4M3) {
@@ -131,23 +135,43 @@ __device__ __forceinline__ void k8_copy_rows(uint32_t dst, const uint8_t* src, i
   }
 }
 
-// Where a unit's parts go: output row r is token t + r / gdiv, head head + r % gdiv.
+// A unit that spans several CTAs, as each of them notes it.  Output row r is token
+// t + r / gdiv, head head + r % gdiv.
 struct K8Join {
-  long long begin, end;  // the unit on the line of chunks; begin < 0: nothing to join
-  long long line;        // length of the line
-  int n;                 // CTAs that share it
+  int n;      // CTAs that hold a part of the unit; 0: nothing to join
+  int first;  // the first of them
+  int slot;   // where its part lies (the others' lies in slot 0)
   int t, head, rows, gdiv;
 };
-// The workspace: a K8Join per CTA (the unit that begins in it and ends in a later one),
-// then two parts per CTA: (maximum, sum) of 16 rows and O [16][DV].
-__host__ __device__ inline size_t k8_parts_at(int n_cta) { return ((size_t)n_cta * sizeof(K8Join) + 255) / 256 * 256; }
+// The workspace: two K8Join per CTA (the unit in whose midst its share begins; the unit
+// that begins in its share and ends behind it), then two parts per CTA, slot 0 the one
+// that its share begins with: (maximum, sum) of 16 rows and O [16][DV].
+__host__ __device__ inline size_t k8_parts_at(int n_cta) {
+  return ((size_t)n_cta * 2 * sizeof(K8Join) + 255) / 256 * 256;
+}
 __host__ __device__ inline size_t k8_part_floats(int dv) { return 32 + 16 * (size_t)dv; }
 
+// n chunks shared evenly over CTAs: the first `rem` of them have one more.
+struct K8Share {
+  long long base;
+  int rem;
+  __device__ long long at(int i) const { return base * i + min(i, rem); }
+  __device__ int of(long long w) const {
+    const long long head = (base + 1) * rem;
+    return (int)(w < head ? w / (base + 1) : rem + (w - head) / base);
+  }
+};
+
 // One output row's four columns from base (maximum - kK8Top), sum and O.
-__device__ __forceinline__ void k8_finish(const K8Fwd& a, int t, int head, int d, float m, float l, float4 o) {
+// sink: its logit times log2(e), -inf for none.
+__device__ __forceinline__ float k8_sink(const K8Fwd& a, int head) {
+  return a.sinks ? __ldg(a.sinks + head) * 1.4426950408889634f : -INFINITY;
+}
+__device__ __forceinline__ void k8_finish(const K8Fwd& a, int t, int head, int d, float sink, float m, float l,
+                                          float4 o) {
   float base = m == -INFINITY ? m : m - kK8Top;
   if (a.sinks) {
-    const float sink = __ldg(a.sinks + head) * 1.4426950408889634f, top = fmaxf(base, sink);
+    const float top = fmaxf(base, sink);
     if (top != -INFINITY) {
       const float f = exp2f(base - top);
       l = l * f + exp2f(sink - top);
@@ -202,71 +226,73 @@ __device__ __forceinline__ K8Span k8_span(const K8Fwd& a, const K8Geom& g, int b
   return r;
 }
 
-__device__ __forceinline__ long long k8_block_sum(long long v, long long* red, int tid) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
-  __syncthreads();
-  if ((tid & 31) == 0) red[tid >> 5] = v;
-  __syncthreads();
-  return red[0] + red[1] + red[2] + red[3];
-}
-
 template <int DK, int DV, bool ROWS, int FMT>
 __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_kernel(const K8Fwd a, float* ws) {
   using P = K8Split<DK, DV, ROWS>;
   constexpr int S = P::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long red[4];
-  __shared__ long long found[2];  // sequence and where it begins on the line
+  __shared__ long long sum[4];
+  __shared__ long long found_at;             // where the share's first sequence begins on the line
+  __shared__ int found[3];                   // that sequence, the unit, the chunk of it
   const K8Cache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, q4 = lane & 3;
   const K8Geom geo = k8_geom(a);
+  pdl_trigger();  // the join waits for this kernel's end, but need not be launched after it
 
   // the line's length, and the sequence that this CTA's share begins in
+  const int per = (c.B + 127) / 128, b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
   long long mine = 0;
-  for (int b = tid; b < c.B; b += 128) {
+  for (int b = b0; b < b1; ++b) {
     const K8Span sp = k8_span(a, geo, b);
     mine += (long long)sp.units * sp.ch;
   }
-  const long long W = k8_block_sum(mine, red, tid);
-  const int n_cta = (int)min(W, (long long)gridDim.x);  // nobody's share is empty but theirs who return
-  const long long w0 = n_cta ? W * blockIdx.x / n_cta : 0, w1 = n_cta ? W * (blockIdx.x + 1) / n_cta : 0;
-  K8Join* joins = reinterpret_cast<K8Join*>(ws);
-  float* parts = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + k8_parts_at(gridDim.x)) +
-                 2 * blockIdx.x * k8_part_floats(DV);
-  if (tid == 0) joins[blockIdx.x].begin = -1;
-  if (blockIdx.x >= n_cta) return;
-  {
-    long long before = 0;
-    for (int b0 = 0; b0 < c.B; b0 += 128) {
-      const int b = b0 + tid;
-      long long n = 0;
-      if (b < c.B) {
-        const K8Span sp = k8_span(a, geo, b);
-        n = (long long)sp.units * sp.ch;
-      }
-      long long inc = n;
+  long long inc = mine;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long x = __shfl_up_sync(~0u, inc, d);
-        if (lane >= d) inc += x;
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(~0u, inc, d);
+    if (lane >= d) inc += x;
+  }
+  if (lane == 31) sum[warp] = inc;
+  __syncthreads();
+  const long long W = sum[0] + sum[1] + sum[2] + sum[3];
+  const int n_cta = (int)min(W, (long long)gridDim.x);  // a share is empty only in CTAs behind these
+  K8Join* const join = reinterpret_cast<K8Join*>(ws) + 2 * blockIdx.x;
+  if (tid < 2) join[tid].n = 0;
+  if (blockIdx.x >= n_cta) return;
+  K8Share share;
+  if (W <= 0x7fffffff) {
+    share.base = (uint32_t)W / (uint32_t)n_cta;
+    share.rem = (int)((uint32_t)W % (uint32_t)n_cta);
+  } else {
+    share.base = W / n_cta;
+    share.rem = (int)(W % n_cta);
+  }
+  const long long w0 = share.at(blockIdx.x), w1 = share.at(blockIdx.x + 1);
+  float* const parts = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + k8_parts_at(gridDim.x)) +
+                       2 * blockIdx.x * k8_part_floats(DV);
+  {
+    long long at = inc - mine;
+    for (int x = 0; x < warp; ++x) at += sum[x];
+    if (at <= w0 && w0 < at + mine) {
+      for (int b = b0;; ++b) {
+        const K8Span sp = k8_span(a, geo, b);
+        const long long n = (long long)sp.units * sp.ch;
+        if (w0 < at + n) {
+          const long long off = w0 - at;
+          const int unit = off <= 0x7fffffff ? (int)((uint32_t)off / (uint32_t)sp.ch) : (int)(off / sp.ch);
+          found_at = at;
+          found[0] = b;
+          found[1] = unit;
+          found[2] = (int)(off - (long long)unit * sp.ch);
+          break;
+        }
+        at += n;
       }
-      __syncthreads();
-      if (lane == 31) red[warp] = inc;
-      __syncthreads();
-      long long at = before + inc - n;
-      for (int w = 0; w < warp; ++w) at += red[w];
-      if (n > 0 && at <= w0 && w0 < at + n) {
-        found[0] = b;
-        found[1] = at;
-      }
-      before += red[0] + red[1] + red[2] + red[3];
-      if (before > w0) break;
     }
     __syncthreads();
   }
-  int b = (int)found[0];
-  long long seq_at = found[1];
+  int b = found[0], unit = found[1], c0 = found[2];
+  long long seq_at = found_at;
   K8Span sp = k8_span(a, geo, b);
 
   const uint32_t sbase = smem_u32(smem) + warp * P::kWarpBytes;
@@ -274,14 +300,12 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
   const int krs = c.Hkv * DK, vrs = c.Hkv * DV;  // bytes from row to row of the cache
 
   for (long long w = w0; w < w1;) {
-    while (w >= seq_at + (long long)sp.units * sp.ch) {  // the next sequence with work
+    while (unit >= sp.units) {  // the next sequence with work
       seq_at += (long long)sp.units * sp.ch;
       sp = k8_span(a, geo, ++b);
+      unit = 0;
     }
-    const long long off = w - seq_at;
-    const int unit = (int)(off / sp.ch), c0 = (int)(off - (long long)unit * sp.ch);
     const int c1 = (int)min((long long)sp.ch, c0 + (w1 - w));
-    const long long unit_at = seq_at + (long long)unit * sp.ch;
     // unit -> (head, tokens, part of the heads); a KV head's units lie together
     const int per_h = sp.units / c.Hkv, h = unit / per_h, ut = unit - h * per_h;
     const int tile = ut / geo.hs, hp = ut - tile * geo.hs;
@@ -297,53 +321,22 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
     if (a.topk && a.topk_len) slots = min(slots, max(0, __ldg(a.topk_len + iu)));
     const int* table = c.table + b * c.tstride;
 
-    // --- Q: this thread's rows gr and gr + 8, as halves times 2^(8 - E) ---------
-    uint32_t qa[DK / 16][4];
-    float fr[2];
+    // --- Q: this thread's rows gr and gr + 8; the loads here, the conversion behind the first copies
+    uint4 raw[2][DK / 32];
     int ta[2], lo[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int row = gr + 8 * r;
-      const int i = min(row / geo.gdiv, ntok - 1);
-      ta[r] = ta0 + i;
+      const int row = gr + 8 * r, tok = row / geo.gdiv;
+      ta[r] = ta0 + min(tok, ntok - 1);
       lo[r] = a.win >= ta[r] ? 0 : ta[r] - a.win;
-      const bool live = row < rows;
       const char* src = static_cast<const char*>(a.q) +
-                        ((long long)(t0 + row / geo.gdiv) * a.qstride + (long long)(head0 + row % geo.gdiv) * DK) * 2;
-      uint4 raw[DK / 32];
-      float big = 0.f;
+                        ((long long)(t0 + tok) * a.qstride + (long long)(head0 + row - tok * geo.gdiv) * DK) * 2;
 #pragma unroll
-      for (int i4 = 0; i4 < DK / 32; ++i4) {
-        // columns 64 * (i4 / 2) + 16 * q4 + 8 * (i4 % 2) ..
-        raw[i4] = live ? __ldg(reinterpret_cast<const uint4*>(src + (64 * (i4 >> 1) + 16 * q4 + 8 * (i4 & 1)) * 2))
-                       : make_uint4(0, 0, 0, 0);
-        const uint32_t v[4] = {raw[i4].x, raw[i4].y, raw[i4].z, raw[i4].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = a.f16 ? __half22float2(*reinterpret_cast<const __half2*>(&v[j]))
-                                 : make_float2(__uint_as_float(v[j] << 16), __uint_as_float(v[j] & 0xffff0000u));
-          big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-      }
-      big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
-      big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
-      const int E = big > 0.f ? max((int)(__float_as_uint(big) >> 23) - 127, -110) : 8;
-      const float mul = __uint_as_float((uint32_t)(8 - E + 127) << 23);
-      fr[r] = a.scale_log2 * __uint_as_float((uint32_t)(E - 8 + 127) << 23);
-#pragma unroll
-      for (int i4 = 0; i4 < DK / 32; ++i4) {
-        const uint32_t v[4] = {raw[i4].x, raw[i4].y, raw[i4].z, raw[i4].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = a.f16 ? __half22float2(*reinterpret_cast<const __half2*>(&v[j]))
-                                 : make_float2(__uint_as_float(v[j] << 16), __uint_as_float(v[j] & 0xffff0000u));
-          const __half2 hh = __floats2half2_rn(f.x * mul, f.y * mul);
-          // column 64 ch + 16 q4 + 4 s + {0, 1 | 2, 3} is k {2 q4, + 1 | + 8, + 9} of step 4 ch + s
-          const int col = 8 * (i4 & 1) + 2 * j, s = (i4 >> 1) * 4 + (col >> 2), up = (col >> 1) & 1;
-          qa[s][r + 2 * up] = *reinterpret_cast<const uint32_t*>(&hh);
-        }
-      }
+      for (int i = 0; i < DK / 32; ++i)  // columns 64 * (i / 2) + 16 * q4 + 8 * (i % 2) ..
+        raw[r][i] = row < rows ? __ldg(reinterpret_cast<const uint4*>(src + (64 * (i >> 1) + 16 * q4 + 8 * (i & 1)) * 2))
+                               : make_uint4(0, 0, 0, 0);
     }
+    const float sink = (tid >> 3) < rows ? k8_sink(a, head0 + (tid >> 3) % geo.gdiv) : -INFINITY;
 
     // --- the steps of this warp: 16 rows of each chunk ----------------------------
     const int n_steps = c1 - c0;
@@ -407,16 +400,6 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
       }
     };
 
-    float o[DV / 16][2][4];
-#pragma unroll
-    for (int i = 0; i < DV / 16; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][e][j] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float base[2] = {0.f, 0.f}, limit[2] = {-INFINITY, -INFINITY};  // m - kK8Top, and how far above it w may lie
-
     int xs[S + 1], rw[S], pg[S];
 #pragma unroll
     for (int k = 0; k <= S; ++k) xs[k] = fetch_idx(k);
@@ -431,6 +414,50 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
       cp_async_commit();
     }
     int next_row = rw[S - 1], next_page = pg[S - 1], next_x = xs[S];
+
+    // Q as halves times 2^(8 - E), E the exponent of the row's largest
+    uint32_t qa[DK / 16][4];
+    float fr[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float big = 0.f;
+#pragma unroll
+      for (int i = 0; i < DK / 32; ++i) {
+        const uint32_t v[4] = {raw[r][i].x, raw[r][i].y, raw[r][i].z, raw[r][i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = k8_two(v[j], a.f16);
+          big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
+      const int E = big > 0.f ? max((int)(__float_as_uint(big) >> 23) - 127, -110) : 8;
+      const float mul = __uint_as_float((uint32_t)(8 - E + 127) << 23);
+      fr[r] = a.scale_log2 * __uint_as_float((uint32_t)(E - 8 + 127) << 23);
+#pragma unroll
+      for (int i = 0; i < DK / 32; ++i) {
+        const uint32_t v[4] = {raw[r][i].x, raw[r][i].y, raw[r][i].z, raw[r][i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = k8_two(v[j], a.f16);
+          const __half2 hh = __floats2half2_rn(f.x * mul, f.y * mul);
+          // column 64 ch + 16 q4 + 4 e + {0, 1 | 2, 3} is k {2 q4, + 1 | + 8, + 9} of step 4 ch + e
+          const int col = 8 * (i & 1) + 2 * j;
+          qa[(i >> 1) * 4 + (col >> 2)][r + 2 * ((col >> 1) & 1)] = *reinterpret_cast<const uint32_t*>(&hh);
+        }
+      }
+    }
+    float o[DV / 16][2][4];
+#pragma unroll
+    for (int i = 0; i < DV / 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][e][j] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float base[2] = {0.f, 0.f}, limit[2] = {-INFINITY, -INFINITY};  // m - kK8Top, and how far above it w may lie
+
 
     int at = 0, fill = S - 1;  // stages of step k and of the one that is fetched
     for (int k = 0; k < n_steps; ++k) {
@@ -636,7 +663,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
       const int row = tid >> 3, part = tid & 7;
       const float* f0 = reinterpret_cast<const float*>(smem);
       constexpr int kW = P::kWarpBytes / 4;
-      float mw[kK8Warps], top = -INFINITY, sum = 0.f;
+      float mw[kK8Warps], top = -INFINITY, total = 0.f;
 #pragma unroll
       for (int x = 0; x < kK8Warps; ++x) {
         mw[x] = f0[x * kW + 16 * P::kLd + row];
@@ -645,7 +672,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
 #pragma unroll
       for (int x = 0; x < kK8Warps; ++x) {
         mw[x] = top == -INFINITY ? 1.f : ex2_approx(mw[x] - top);
-        sum = fmaf(f0[x * kW + 16 * P::kLd + 16 + row], mw[x], sum);
+        total = fmaf(f0[x * kW + 16 * P::kLd + 16 + row], mw[x], total);
       }
       const bool whole = c0 == 0 && c1 == sp.ch;
       // a part of a unit: slot 0 holds the one that this CTA's share begins with
@@ -664,86 +691,93 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
             v.z = fmaf(y.z, mw[x], v.z);
             v.w = fmaf(y.w, mw[x], v.w);
           }
-          if (whole) k8_finish(a, t, head, d, top, sum, v);
+          if (whole) k8_finish(a, t, head, d, sink, top, total, v);
           else *reinterpret_cast<float4*>(part_out + 32 + row * DV + d) = v;
         }
         if (!whole && part == 0) {
           part_out[row] = top;
-          part_out[16 + row] = sum;
+          part_out[16 + row] = total;
         }
       }
-      if (!whole && c0 == 0 && tid == 0) {
+      if (!whole && tid == 0) {
+        const long long begin = seq_at + (long long)unit * sp.ch;
         K8Join jn;
-        jn.begin = unit_at;
-        jn.end = unit_at + sp.ch;
-        jn.line = W;
-        jn.n = n_cta;
+        jn.first = c0 == 0 ? blockIdx.x : share.of(begin);
+        jn.n = share.of(begin + sp.ch - 1) - jn.first + 1;
+        jn.slot = share.at(jn.first) == begin ? 0 : 1;
         jn.t = t0;
         jn.head = head0;
         jn.rows = rows;
         jn.gdiv = geo.gdiv;
-        joins[blockIdx.x] = jn;
+        join[c0 == 0] = jn;
       }
     }
     __syncthreads();  // the stages are filled again
     w += c1 - c0;
+    c0 = 0;
+    ++unit;
   }
 }
 
-// The units that span several CTAs: blocks 4 i .. 4 i + 3 join the rows of the unit that
-// begins in CTA i's share and ends behind it.  Its part in CTA x lies in slot 0 where the
-// share of x begins inside the unit (or with it), else in slot 1.  A row takes four
-// warps, each over a quarter of the parts, in a fixed order.
+// The units that span several CTAs.  The n blocks that held a part of a unit share its
+// rows: block x of them takes rows x, x + n, ...  Up to 8 parts, a warp sums a row's;
+// more, the 8 warps take an eighth of a row's parts each.  The order is fixed.
 template <int DV>
-__global__ void __launch_bounds__(512) k8_join_kernel(const K8Fwd a, const float* ws, int n_grid) {
-  __shared__ float sl[16];
-  __shared__ float4 so[16][DV / 4];
+__global__ void __launch_bounds__(256) k8_join_kernel(const K8Fwd a, const float* ws, int n_grid) {
+  __shared__ float sl[8];
+  __shared__ float4 so[8][DV / 4];
   pdl_wait();
-  const int i = blockIdx.x >> 2, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const K8Join jn = reinterpret_cast<const K8Join*>(ws)[i];
-  if (jn.begin < 0) return;
-  const int row = (blockIdx.x & 3) * 4 + (warp >> 2);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float* parts = reinterpret_cast<const float*>(reinterpret_cast<const char*>(ws) + k8_parts_at(n_grid));
-  const int first = 2 * i + (jn.line * i / jn.n == jn.begin ? 0 : 1);
-  const int n = (int)((jn.end * jn.n + jn.line - 1) / jn.line) - i;  // parts: of CTAs i .. i + n - 1
-  auto part = [&](int x) { return parts + (x ? 2 * (i + x) : first) * k8_part_floats(DV); };
-  const bool live = row < jn.rows;
-  float top = -INFINITY, sum = 0.f;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (live) {
-    for (int x = lane; x < n; x += 32) top = fmaxf(top, part(x)[row]);
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const K8Join jn = reinterpret_cast<const K8Join*>(ws)[2 * blockIdx.x + which];
+    if (jn.n == 0) continue;
+    const int step = jn.n <= 8 ? 1 : 8, mine = blockIdx.x - jn.first;
+    for (int row = mine + (step == 1 ? warp * jn.n : 0); row < jn.rows; row += step == 1 ? 8 * jn.n : jn.n) {
+      auto part = [&](int x) { return parts + (2 * (jn.first + x) + (x ? 0 : jn.slot)) * k8_part_floats(DV); };
+      const int head = jn.head + row % jn.gdiv;
+      const float sink = k8_sink(a, head);
+      float top = -INFINITY, sum = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int x = lane; x < jn.n; x += 32) top = fmaxf(top, __ldcg(part(x) + row));
 #pragma unroll
-    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
 #pragma unroll 4
-    for (int x = warp & 3; x < n; x += 4) {
-      const float* p = part(x);
-      const float f = top == -INFINITY ? 1.f : ex2_approx(p[row] - top);
-      sum = fmaf(p[16 + row], f, sum);
-      if (lane < DV / 4) {
-        const float4 y = *reinterpret_cast<const float4*>(p + 32 + row * DV + 4 * lane);
-        v.x = fmaf(y.x, f, v.x);
-        v.y = fmaf(y.y, f, v.y);
-        v.z = fmaf(y.z, f, v.z);
-        v.w = fmaf(y.w, f, v.w);
+      for (int x = step == 1 ? 0 : warp; x < jn.n; x += step) {
+        const float* p = part(x);
+        const float f = top == -INFINITY ? 1.f : ex2_approx(__ldcg(p + row) - top);
+        sum = fmaf(__ldcg(p + 16 + row), f, sum);
+        if (lane < DV / 4) {
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(p + 32 + row * DV) + lane);
+          v.x = fmaf(y.x, f, v.x);
+          v.y = fmaf(y.y, f, v.y);
+          v.z = fmaf(y.z, f, v.z);
+          v.w = fmaf(y.w, f, v.w);
+        }
       }
-    }
-    if (lane == 0) sl[warp] = sum;
-    if (lane < DV / 4) so[warp][lane] = v;
-  }
-  __syncthreads();
-  if (!live || (warp & 3) || lane >= DV / 4) return;
-  sum = 0.f;
-  v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (step == 8) {
+        if (lane == 0) sl[warp] = sum;
+        if (lane < DV / 4) so[warp][lane] = v;
+        __syncthreads();
+        if (warp == 0) {
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    sum += sl[warp + x];
-    const float4 y = so[warp + x][lane];
-    v.x += y.x;
-    v.y += y.y;
-    v.z += y.z;
-    v.w += y.w;
+          for (int x = 1; x < 8; ++x) {
+            sum += sl[x];
+            if (lane < DV / 4) {
+              const float4 y = so[x][lane];
+              v.x += y.x;
+              v.y += y.y;
+              v.z += y.z;
+              v.w += y.w;
+            }
+          }
+        }
+      }
+      if ((step == 1 || warp == 0) && lane < DV / 4) k8_finish(a, jn.t + row / jn.gdiv, head, 4 * lane, sink, top, sum, v);
+      if (step == 8) __syncthreads();  // sl, so
+    }
   }
-  k8_finish(a, jn.t + row / jn.gdiv, jn.head + row % jn.gdiv, 4 * lane, top, sum, v);
 }
 
 // CTAs of the split kernel: all that the SMs hold at once, or as many as the longest
@@ -772,7 +806,7 @@ static cudaError_t split_t(const K8Fwd& a, void* ws, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess || n == 1) return e;
   count_launch();
-  return launch_pdl(k8_join_kernel<DV>, 4u * n, 512, 0, st, a, (const float*)ws, n);
+  return launch_pdl(k8_join_kernel<DV>, (unsigned)n, 256, 0, st, a, (const float*)ws, n);
 }
 
 template <int DK, int DV>
