@@ -51,6 +51,10 @@ struct K8Fwd {
   K8Cache c;
   int f16, Hq, G, bs, topk;
   K8Div by_bs;
+  // the units of query rows that the split kernel works on: tokens per unit, query rows of a
+  // token in a unit, units over a token's heads, and chunks of a unit that selects (0: every row)
+  int tpt, gdiv, hs, sel_ch;
+  K8Div by_tpt, by_gdiv;
   int win;           // rows before the token's own that it sees (INT_MAX: all)
   float scale_log2;  // scale * log2(e)
   const void* q;
@@ -73,7 +77,7 @@ struct PagePlan {
 cudaError_t launch_page_plan(const PagePlan& p, cudaStream_t st);
 cudaError_t launch_kv8_write(K8Write a, cudaStream_t st);
 bool k8_built(int dqk, int dv, bool shared);
-size_t k8_fwd_workspace(const K8Fwd& a);
-cudaError_t launch_kv8_fwd(const K8Fwd& a, void* ws, cudaStream_t st);
+size_t k8_fwd_workspace(K8Fwd a);
+cudaError_t launch_kv8_fwd(K8Fwd a, void* ws, cudaStream_t st);
 
 }  // namespace sa

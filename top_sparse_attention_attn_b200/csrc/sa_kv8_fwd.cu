@@ -1,9 +1,11 @@
 // sa_kv8_fwd.cu -- attention over a paged KV cache held in 8 bits (sa_kv8_fwd).
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "sa_kv8_device.cuh"
 #include "sa_launch.h"
+#include "sa_tc.cuh"
 
 namespace sa {
 
@@ -39,23 +41,33 @@ constexpr float kK8Grow = 4.f, kK8Top = 11.f;
 
 template <int DK, int DV, bool ROWS>
 struct K8Split {
+  static constexpr int kData = 16 * (DK + DV);
   static constexpr int kMeta = ROWS ? 192 : 16;  // scales and rows of a step
-  static constexpr int kStage = 16 * (DK + DV) + kMeta;
   static constexpr int kStages = DK + DV <= 128 ? 6 : 4;
-  static constexpr int kWarpBytes = kStage * kStages;
-  static constexpr int kSmem = kWarpBytes * kK8Warps;
   static constexpr int kOcc = DK + DV <= 128 ? 4 : (DK <= 128 ? 3 : 2);
+  static constexpr int kMetaAt = kK8Warps * kStages * kData;
+  static constexpr int kBarAt = kMetaAt + kK8Warps * kStages * kMeta;
+  static constexpr int kSmem = kBarAt + kK8Warps * kStages * 8 + 1024;  // the swizzles want 1024-byte alignment
   static constexpr int kLd = DV + 16;  // O in shared memory: rows 16 banks apart
-  static_assert(16 * kLd * 4 + 128 <= kWarpBytes, "the warps' results must fit in their stages");
+  static_assert(16 * kLd * 4 + 128 <= kStages * kData, "a warp's result must fit in its stages");
+};
+struct K8Maps {
+  CUtensorMap k, k2, v;  // columns 0 .. 127 (or 63) of K, columns 128 .. 191, V
 };
 
-// 16-byte piece of a row after the swizzle: 8 rows' same piece, and two rows' four
-// neighbouring pieces, fall on different banks.
+// Byte of 16-byte piece p of row r in a step's 16 rows, as the TMA swizzles lay them.
 template <int D>
-__device__ __forceinline__ int k8_piece(int r, int c) {
-  if (D == 128) return c ^ (((r & 1) << 2) | ((r >> 1) & 3));
-  if (D == 64) return c ^ ((r >> 1) & 3);
-  return c;
+__device__ __forceinline__ int k8_at(int r, int p) {
+  if (D == 64) return r * 64 + ((p ^ ((r >> 1) & 3)) << 4);
+  if (D == 128) return r * 128 + ((p ^ (r & 7)) << 4);
+  return p < 8 ? r * 128 + ((p ^ (r & 7)) << 4) : 2048 + r * 64 + (((p - 8) ^ ((r >> 1) & 3)) << 4);
+}
+// The MMA's row n of 8 is row k8_row(n) of the step, so that the 16-byte reads of two
+// rows' four neighbouring pieces fall on different banks: rows r and r + 4 of 128
+// bytes, rows r and r + 1 of 64.
+template <int DK>
+__device__ __forceinline__ int k8_row(int n) {
+  return DK == 64 ? n : (n >> 1) | ((n & 1) << 2);
 }
 
 __device__ __forceinline__ float2 k8_two(uint32_t v, int f16) {
@@ -115,14 +127,12 @@ __device__ __forceinline__ float k8_log2(float x) {
   return r;
 }
 
-// 16 rows of D bytes, `rs` bytes apart, to shared memory; with EDGE, rows outside [lo, hi) are zeros.
-template <int D, bool EDGE>
-__device__ __forceinline__ void k8_copy_step(uint32_t dst, const uint8_t* src, int rs, int lane, int lo, int hi) {
-#pragma unroll
-  for (int it = 0; it < D / 32; ++it) {
-    const int i = it * 32 + lane, r = i / (D / 16), pc = i - r * (D / 16);
-    cp_async16(dst + r * D + k8_piece<D>(r, pc) * 16, src + r * rs + pc * 16, !EDGE || (r >= lo && r < hi));
-  }
+__device__ __forceinline__ void k8_box(uint32_t dst, const CUtensorMap* map, int head, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(head), "r"(row), "r"(bar)
+      : "memory");
 }
 // 16 rows of which lane r holds the row of the cache (negative: zeros)
 template <int D>
@@ -131,7 +141,7 @@ __device__ __forceinline__ void k8_copy_rows(uint32_t dst, const uint8_t* src, i
   for (int it = 0; it < D / 32; ++it) {
     const int i = it * 32 + lane, r = i / (D / 16), pc = i - r * (D / 16);
     const int at = __shfl_sync(~0u, rr, r);
-    cp_async16(dst + r * D + k8_piece<D>(r, pc) * 16, src + (long long)(at >= 0 ? at : 0) * rs + pc * 16, at >= 0);
+    cp_async16(dst + k8_at<D>(r, pc), src + (long long)(at >= 0 ? at : 0) * rs + pc * 16, at >= 0);
   }
 }
 
@@ -162,88 +172,86 @@ struct K8Share {
   }
 };
 
-// One output row's four columns from base (maximum - kK8Top), sum and O.
-// sink: its logit times log2(e), -inf for none.
+// sink: a head's sink logit times log2(e), -inf for none.
 __device__ __forceinline__ float k8_sink(const K8Fwd& a, int head) {
   return a.sinks ? __ldg(a.sinks + head) * 1.4426950408889634f : -INFINITY;
 }
-__device__ __forceinline__ void k8_finish(const K8Fwd& a, int t, int head, int d, float sink, float m, float l,
-                                          float4 o) {
-  float base = m == -INFINITY ? m : m - kK8Top;
-  if (a.sinks) {
+// What an output row's O is multiplied by, from its maximum, sum and sink; and its lse.
+__device__ __forceinline__ float k8_norm(float sink, float m, float l, float* lse) {
+  float base = m == -INFINITY ? m : m - kK8Top, f = 1.f;
+  if (sink != -INFINITY) {
     const float top = fmaxf(base, sink);
-    if (top != -INFINITY) {
-      const float f = exp2f(base - top);
-      l = l * f + exp2f(sink - top);
-      o.x *= f; o.y *= f; o.z *= f; o.w *= f;
-      base = top;
-    }
+    f = ex2_approx(base - top);
+    l = l * f + ex2_approx(sink - top);
+    base = top;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const long long row = (long long)t * a.Hq + head;
+  *lse = l == 0.f ? INFINITY : 0.6931471805599453f * (base + log2f(l));
+  return l == 0.f ? 0.f : f / l;
+}
+__device__ __forceinline__ void k8_store(const K8Fwd& a, int t, int head, int d, float f, float4 o) {
   uint2 out;
   if (a.f16) {
-    const __half2 x = __floats2half2_rn(o.x * inv, o.y * inv), y = __floats2half2_rn(o.z * inv, o.w * inv);
+    const __half2 x = __floats2half2_rn(o.x * f, o.y * f), y = __floats2half2_rn(o.z * f, o.w * f);
     out = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
   } else {
-    out = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    out = make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
   }
-  *reinterpret_cast<uint2*>(static_cast<char*>(a.o) + (row * a.c.dv + d) * 2) = out;
-  if (d == 0) a.lse[row] = l == 0.f ? INFINITY : 0.6931471805599453f * (base + log2f(l));
-}
-
-struct K8Geom {
-  int tpt;     // tokens per unit
-  int hs;      // units over a token's heads
-  int gdiv;    // query rows of a token in a unit
-  int sel_ch;  // chunks of a unit that selects (0: every row)
-};
-__host__ __device__ inline K8Geom k8_geom(const K8Fwd& a) {
-  K8Geom g;
-  g.gdiv = a.G < 16 ? a.G : 16;
-  g.hs = (a.G + 15) / 16;
-  g.tpt = a.topk || a.G > 16 ? 1 : 16 / a.G;
-  g.sel_ch = a.topk ? (int)(((long long)a.topk * a.bs + kK8Chunk - 1) / kK8Chunk) : 0;
-  return g;
+  *reinterpret_cast<uint2*>(static_cast<char*>(a.o) + (((long long)t * a.Hq + head) * a.c.dv + d) * 2) = out;
 }
 
 // units and chunks per unit of a sequence
 struct K8Span {
   K8Seq s;
   int units, ch;
+  int per_h;  // units of a KV head
 };
-__device__ __forceinline__ K8Span k8_span(const K8Fwd& a, const K8Geom& g, int b) {
+__device__ __forceinline__ K8Span k8_span(const K8Fwd& a, int b) {
   K8Span r;
   r.s = k8_seq(a.c, b);
-  r.units = (r.s.n + g.tpt - 1) / g.tpt * g.hs * a.c.Hkv;
-  if (g.sel_ch) {
-    r.ch = g.sel_ch;
+  r.per_h = k8_quot(a.by_tpt, r.s.n + a.tpt - 1) * a.hs;
+  r.units = r.per_h * a.c.Hkv;
+  if (a.sel_ch) {
+    r.ch = a.sel_ch;
   } else {
     r.ch = max((r.s.L + kK8Chunk - 1) / kK8Chunk, 1);
     // a window: from the step of 16 that its first row lies in
-    if (a.win < (1 << 29)) r.ch = min(r.ch, (a.win + g.tpt + 15 + kK8Chunk - 1) / kK8Chunk);
+    if (a.win < (1 << 29)) r.ch = min(r.ch, (a.win + a.tpt + 15 + kK8Chunk - 1) / kK8Chunk);
   }
   return r;
 }
 
 template <int DK, int DV, bool ROWS, int FMT>
-__global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_kernel(const K8Fwd a, float* ws) {
+__global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc)
+    k8_split_kernel(const __grid_constant__ K8Fwd a, const __grid_constant__ K8Maps maps, float* ws) {
   using P = K8Split<DK, DV, ROWS>;
   constexpr int S = P::kStages;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023);
   __shared__ long long sum[4];
-  __shared__ long long found_at;             // where the share's first sequence begins on the line
-  __shared__ int found[3];                   // that sequence, the unit, the chunk of it
+  __shared__ long long found_at;  // where the share's first sequence begins on the line
+  __shared__ int found[4];        // that sequence, the head, the unit of the head, the chunk
+  __shared__ K8Span found_span;
+  __shared__ int dead_word;
   const K8Cache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, q4 = lane & 3;
-  const K8Geom geo = k8_geom(a);
+  if (tid == 0) dead_word = 0;
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + P::kBarAt) + warp * S;
+  if (!ROWS) {
+    if (lane < S) mbar_init(bars + lane, 1);
+    mbar_fence_init();
+    if (tid == 0) {
+      tma_prefetch_desc(&maps.k);
+      tma_prefetch_desc(&maps.v);
+    }
+  }
   pdl_trigger();  // the join waits for this kernel's end, but need not be launched after it
 
   // the line's length, and the sequence that this CTA's share begins in
   const int per = (c.B + 127) / 128, b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
   long long mine = 0;
+  K8Span sp = {};
   for (int b = b0; b < b1; ++b) {
-    const K8Span sp = k8_span(a, geo, b);
+    sp = k8_span(a, b);
     mine += (long long)sp.units * sp.ch;
   }
   long long inc = mine;
@@ -275,15 +283,17 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
     for (int x = 0; x < warp; ++x) at += sum[x];
     if (at <= w0 && w0 < at + mine) {
       for (int b = b0;; ++b) {
-        const K8Span sp = k8_span(a, geo, b);
+        if (b1 - b0 > 1) sp = k8_span(a, b);
         const long long n = (long long)sp.units * sp.ch;
         if (w0 < at + n) {
           const long long off = w0 - at;
           const int unit = off <= 0x7fffffff ? (int)((uint32_t)off / (uint32_t)sp.ch) : (int)(off / sp.ch);
           found_at = at;
+          found_span = sp;
           found[0] = b;
-          found[1] = unit;
-          found[2] = (int)(off - (long long)unit * sp.ch);
+          found[1] = (uint32_t)unit / (uint32_t)sp.per_h;
+          found[2] = unit - found[1] * sp.per_h;
+          found[3] = (int)(off - (long long)unit * sp.ch);
           break;
         }
         at += n;
@@ -291,27 +301,29 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
     }
     __syncthreads();
   }
-  int b = found[0], unit = found[1], c0 = found[2];
+  int b = found[0], h = found[1], ut = found[2], c0 = found[3];
   long long seq_at = found_at;
-  K8Span sp = k8_span(a, geo, b);
+  sp = found_span;
 
-  const uint32_t sbase = smem_u32(smem) + warp * P::kWarpBytes;
-  uint8_t* const wsm = smem + warp * P::kWarpBytes;
+  uint8_t* const wsm = smem + warp * S * P::kData;
+  uint8_t* const wmeta = smem + P::kMetaAt + warp * S * P::kMeta;
+  const uint32_t sbase = smem_u32(wsm), mbase = smem_u32(wmeta), bar0 = smem_u32(bars);
+  uint32_t phases = 0;  // of this warp's barriers
+  int dead = 0;         // a wait gave up: no more copies, and NaN for a result
   const int krs = c.Hkv * DK, vrs = c.Hkv * DV;  // bytes from row to row of the cache
 
   for (long long w = w0; w < w1;) {
-    while (unit >= sp.units) {  // the next sequence with work
+    while (h >= c.Hkv || sp.units == 0) {  // the next sequence with work
       seq_at += (long long)sp.units * sp.ch;
-      sp = k8_span(a, geo, ++b);
-      unit = 0;
+      sp = k8_span(a, ++b);
+      h = 0;
     }
     const int c1 = (int)min((long long)sp.ch, c0 + (w1 - w));
-    // unit -> (head, tokens, part of the heads); a KV head's units lie together
-    const int per_h = sp.units / c.Hkv, h = unit / per_h, ut = unit - h * per_h;
-    const int tile = ut / geo.hs, hp = ut - tile * geo.hs;
-    const int t0 = sp.s.t0 + tile * geo.tpt, ntok = min(geo.tpt, sp.s.n - tile * geo.tpt);
-    const int head0 = h * a.G + hp * 16, rows = geo.hs > 1 ? min(16, a.G - hp * 16) : ntok * a.G;
-    const int ta0 = sp.s.first + tile * geo.tpt, ta1 = ta0 + ntok - 1;  // rows of the first and last token
+    // a KV head's units lie together, a token's parts of the heads innermost
+    const int tile = a.hs == 1 ? ut : ut / a.hs, hp = ut - tile * a.hs;
+    const int t0 = sp.s.t0 + tile * a.tpt, ntok = min(a.tpt, sp.s.n - tile * a.tpt);
+    const int head0 = h * a.G + hp * 16, rows = a.hs > 1 ? min(16, a.G - hp * 16) : ntok * a.G;
+    const int ta0 = sp.s.first + tile * a.tpt, ta1 = ta0 + ntok - 1;  // rows of the first and last token
     const int lo_all = a.win >= ta0 ? 0 : ta0 - a.win, hi_all = min(ta1 + 1, sp.s.L);
     const int lo_last = a.win >= ta1 ? 0 : ta1 - a.win;
     const int start = lo_all & ~15;
@@ -326,17 +338,17 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
     int ta[2], lo[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int row = gr + 8 * r, tok = row / geo.gdiv;
+      const int row = gr + 8 * r, tok = k8_quot(a.by_gdiv, row);
       ta[r] = ta0 + min(tok, ntok - 1);
       lo[r] = a.win >= ta[r] ? 0 : ta[r] - a.win;
       const char* src = static_cast<const char*>(a.q) +
-                        ((long long)(t0 + tok) * a.qstride + (long long)(head0 + row - tok * geo.gdiv) * DK) * 2;
+                        ((long long)(t0 + tok) * a.qstride + (long long)(head0 + row - tok * a.gdiv) * DK) * 2;
 #pragma unroll
       for (int i = 0; i < DK / 32; ++i)  // columns 64 * (i / 2) + 16 * q4 + 8 * (i % 2) ..
         raw[r][i] = row < rows ? __ldg(reinterpret_cast<const uint4*>(src + (64 * (i >> 1) + 16 * q4 + 8 * (i & 1)) * 2))
                                : make_uint4(0, 0, 0, 0);
     }
-    const float sink = (tid >> 3) < rows ? k8_sink(a, head0 + (tid >> 3) % geo.gdiv) : -INFINITY;
+    const float sink = (tid >> 3) < rows ? k8_sink(a, head0 + k8_rem(a.by_gdiv, tid >> 3)) : -INFINITY;
 
     // --- the steps of this warp: 16 rows of each chunk ----------------------------
     const int n_steps = c1 - c0;
@@ -367,35 +379,31 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
         if (c.status) atomicOr(c.status, kStatusIndexRange);
         row = -1;
       }
-      const uint32_t dst = sbase + st * P::kStage, meta = dst + 16 * (DK + DV);
-      int* im = reinterpret_cast<int*>(wsm + st * P::kStage + 16 * (DK + DV));
+      const uint32_t dst = sbase + st * P::kData, meta = mbase + st * P::kMeta;
+      int* im = reinterpret_cast<int*>(wmeta + st * P::kMeta);
       const int rr = row >= 0 ? page * c.ps + k8_rem(c.by_ps, row) : -1;  // row of the cache
+      const float* ks = c.ks + (long long)page * c.Hkv + h;
+      const float* vs = c.vs + (long long)page * c.Hkv + h;
       if (ROWS) {
         if (lane < 16) {
           im[lane] = row;
           if (row >= 0) {
-            k8_cp4(meta + 64 + 4 * lane, c.ks + (long long)page * c.Hkv + h);
-            k8_cp4(meta + 128 + 4 * lane, c.vs + (long long)page * c.Hkv + h);
+            k8_cp4(meta + 64 + 4 * lane, ks);
+            k8_cp4(meta + 128 + 4 * lane, vs);
           }
         }
-      } else {
-        if (lane == 2) im[2] = row;
-        if (row < 0) return;
-        if (lane == 0) k8_cp4(meta, c.ks + (long long)page * c.Hkv + h);
-        if (lane == 1) k8_cp4(meta + 4, c.vs + (long long)page * c.Hkv + h);
-      }
-      if (ROWS) {
         k8_copy_rows<DK>(dst, c.k + h * DK, krs, rr, lane);
         k8_copy_rows<DV>(dst + 16 * DK, c.v + h * DV, vrs, rr, lane);
-      } else {
-        const uint8_t* ksrc = c.k + (long long)rr * krs + h * DK;
-        const uint8_t* vsrc = c.v + (long long)rr * vrs + h * DV;
-        if (row >= lo_all && row + 16 <= hi_all) {
-          k8_copy_step<DK, false>(dst, ksrc, krs, lane, 0, 16);
-          k8_copy_step<DV, false>(dst + 16 * DK, vsrc, vrs, lane, 0, 16);
-        } else {  // zeros in the rows that none of the unit's tokens sees
-          k8_copy_step<DK, true>(dst, ksrc, krs, lane, lo_all - row, hi_all - row);
-          k8_copy_step<DV, true>(dst + 16 * DK, vsrc, vrs, lane, lo_all - row, hi_all - row);
+      } else if (lane == 0) {
+        im[2] = row;
+        if (row >= 0) {
+          k8_cp4(meta, ks);
+          k8_cp4(meta + 4, vs);
+          const uint32_t bar = bar0 + st * 8;
+          mbar_arrive_tx(bars + st, P::kData);
+          k8_box(dst, &maps.k, h, rr, bar);
+          if (DK == 192) k8_box(dst + 2048, &maps.k2, h, rr, bar);
+          k8_box(dst + 16 * DK, &maps.v, h, rr, bar);
         }
       }
     };
@@ -410,7 +418,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
     }
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) {
-      issue(k, rw[k], pg[k]);
+      if (!dead) issue(k, rw[k], pg[k]);
       cp_async_commit();
     }
     int next_row = rw[S - 1], next_page = pg[S - 1], next_x = xs[S];
@@ -463,19 +471,28 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
     for (int k = 0; k < n_steps; ++k) {
       k8_cp_wait<S - 2>();
       __syncwarp();
-      issue(fill, next_row, next_page);
+      if (!dead) issue(fill, next_row, next_page);
       cp_async_commit();
       next_row = resolve(k + S, next_x);
       next_page = fetch_page(next_row);
       next_x = fetch_idx(k + S + 1);
 
-      uint8_t* const st = wsm + at * P::kStage;
-      const uint32_t sv = sbase + at * P::kStage + 16 * DK;
+      uint8_t* const st = wsm + at * P::kData;
+      const uint32_t sv = sbase + at * P::kData + 16 * DK;
+      const int* im = reinterpret_cast<const int*>(wmeta + at * P::kMeta);
+      const int row0 = ROWS ? 0 : im[2], bit = at;
       fill = at;
       at = at + 1 == S ? 0 : at + 1;
-      const int* im = reinterpret_cast<const int*>(st + 16 * (DK + DV));
-      const int row0 = ROWS ? 0 : im[2];
-      if (!ROWS && row0 < 0) continue;
+      if (!ROWS) {
+        if (row0 < 0 || dead) continue;
+        const uint32_t parity = (phases >> bit) & 1;
+        if (!__all_sync(~0u, mbar_try_wait(bars + bit, parity)) &&
+            !__all_sync(~0u, mbar_wait(bars + bit, parity, &dead_word, c.status))) {
+          dead = 1;
+          continue;
+        }
+        phases ^= 1u << bit;
+      }
       if (ROWS && __all_sync(~0u, im[lane & 15] < 0)) continue;
 
       // scores of 16 rows
@@ -484,8 +501,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
       for (int ch = 0; ch < DK / 64; ++ch)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int r = 8 * j + gr;
-          const uint4 kw = *reinterpret_cast<const uint4*>(st + r * DK + k8_piece<DK>(r, ch * 4 + q4) * 16);
+          const uint4 kw = *reinterpret_cast<const uint4*>(st + k8_at<DK>(8 * j + k8_row<DK>(gr), ch * 4 + q4));
           const uint32_t v[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -516,7 +532,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int pos = row0 + 8 * j + 2 * q4 + (e & 1);
+              const int pos = row0 + 8 * j + k8_row<DK>(2 * q4 + (e & 1));
               if (pos > ta[e >> 1] || pos < lo[e >> 1]) s[j][e] = -INFINITY;
             }
         }
@@ -526,7 +542,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int col = 8 * j + 2 * q4 + e, pos = im[col];
+            const int col = 8 * j + k8_row<DK>(2 * q4 + e), pos = im[col];
             const float ks = k8_scale(fm[16 + col]), vs = k8_scale(fm[32 + col]), lv = k8_log2(vs);
             iv[j][e] = k8_rcp(vs);
             s[j][e] = pos >= 0 && pos <= ta[0] && pos >= lo[0] ? fmaf(s[j][e], fr[0] * ks, lv - base[0]) : -INFINITY;
@@ -534,23 +550,25 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
                 pos >= 0 && pos <= ta[1] && pos >= lo[1] ? fmaf(s[j][e + 2], fr[1] * ks, lv - base[1]) : -INFINITY;
           }
       }
-      if (FMT == kFmtE4M3 && !full && ntok > 1) {
-        // A NaN in a V row that some of the unit's tokens see and others do not: the
-        // product would carry it (0 * NaN) to all of them.  It is set into the rows that
-        // see it here, and out of the tile.
-        bool nan = false;
-        for (int i = lane; i < 4 * DV; i += 32) {
-          const uint32_t v = reinterpret_cast<const uint32_t*>(st + 16 * DK)[i];
-          nan = nan || __vcmpeq4(v & 0x7f7f7f7fu, 0x7f7f7f7fu);
+      if (FMT == kFmtE4M3 && !full) {
+        // A NaN in a V row that some of the unit's rows do not see (a stale row of the page,
+        // a later token's): the product would carry it (0 * NaN) to all of them.  It is set
+        // into the rows that see it here, and out of the tile.
+        uint32_t nan = 0;
+#pragma unroll
+        for (int i = 0; i < DV / 32; ++i) {
+          const uint4 v = *reinterpret_cast<const uint4*>(st + 16 * DK + (i * 32 + lane) * 16);
+          nan |= ((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) |
+                 ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u);
         }
-        if (__any_sync(~0u, nan)) {
+        if (__any_sync(~0u, nan & 0x80808080u)) {
+#pragma unroll 1
           for (int r = 0; r < 16; ++r) {
             const int pos = ROWS ? im[r] : row0 + r;
             const bool see[2] = {pos >= 0 && pos <= ta[0] && pos >= lo[0], pos >= 0 && pos <= ta[1] && pos >= lo[1]};
 #pragma unroll
             for (int pc = 0; pc < DV / 16; ++pc) {
-              const uint32_t v =
-                  *reinterpret_cast<const uint32_t*>(st + 16 * DK + r * DV + k8_piece<DV>(r, pc) * 16 + 4 * q4);
+              const uint32_t v = *reinterpret_cast<const uint32_t*>(st + 16 * DK + k8_at<DV>(r, pc) + 4 * q4);
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 if (((v >> (8 * x)) & 0x7f) != 0x7f) continue;
@@ -564,6 +582,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
             uint32_t* v = reinterpret_cast<uint32_t*>(st + 16 * DK) + i;
             *v &= ~__vcmpeq4(*v & 0x7f7f7f7fu, 0x7f7f7f7fu);
           }
+          fence_async_smem();  // the next copy into this stage comes behind these writes
           __syncwarp();
         }
       }
@@ -627,8 +646,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
 #pragma unroll
       for (int pc = 0; pc < DV / 16; pc += 2) {
         uint32_t v[4];
-        const int r = (lane & 7) + (lane & 8), p = pc + (lane >> 4);
-        ldsm_x4_t(v, sv + r * DV + k8_piece<DV>(r, p) * 16);
+        ldsm_x4_t(v, sv + k8_at<DV>(k8_row<DK>(lane & 7) + (lane & 8), pc + (lane >> 4)));
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           uint32_t e0, o0, e1, o1;
@@ -640,6 +658,11 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
       }
     }
     k8_cp_wait<0>();
+    if (dead) {
+      if (!ROWS)
+        for (int i = 0; i < S; ++i) mbar_wait_drain(bars + i, (phases >> i) & 1);
+      l[0] = l[1] = __int_as_float(0x7fffffff);
+    }
     __syncwarp();
 
     // --- the warps' results meet: maximum, sum, O --------------------------------
@@ -662,7 +685,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
     {
       const int row = tid >> 3, part = tid & 7;
       const float* f0 = reinterpret_cast<const float*>(smem);
-      constexpr int kW = P::kWarpBytes / 4;
+      constexpr int kW = S * P::kData / 4;
       float mw[kK8Warps], top = -INFINITY, total = 0.f;
 #pragma unroll
       for (int x = 0; x < kK8Warps; ++x) {
@@ -678,7 +701,10 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
       // a part of a unit: slot 0 holds the one that this CTA's share begins with
       float* part_out = parts + (w == w0 ? 0 : k8_part_floats(DV));
       if (row < rows) {
-        const int t = t0 + row / geo.gdiv, head = head0 + row % geo.gdiv;
+        const int tok = k8_quot(a.by_gdiv, row), t = t0 + tok, head = head0 + row - tok * a.gdiv;
+        float lse, norm = 0.f;
+        if (whole) norm = k8_norm(sink, top, total, &lse);
+        if (whole && part == 0) a.lse[(long long)t * a.Hq + head] = lse;
 #pragma unroll
         for (int i = 0; i < DV / 32; ++i) {
           const int d = 4 * (part + 8 * i);
@@ -691,7 +717,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
             v.z = fmaf(y.z, mw[x], v.z);
             v.w = fmaf(y.w, mw[x], v.w);
           }
-          if (whole) k8_finish(a, t, head, d, sink, top, total, v);
+          if (whole) k8_store(a, t, head, d, norm, v);
           else *reinterpret_cast<float4*>(part_out + 32 + row * DV + d) = v;
         }
         if (!whole && part == 0) {
@@ -700,22 +726,26 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc) k8_split_ker
         }
       }
       if (!whole && tid == 0) {
-        const long long begin = seq_at + (long long)unit * sp.ch;
+        const long long begin = seq_at + ((long long)h * sp.per_h + ut) * sp.ch;
         K8Join jn;
-        jn.first = c0 == 0 ? blockIdx.x : share.of(begin);
+        jn.first = c0 == 0 ? (int)blockIdx.x : share.of(begin);
         jn.n = share.of(begin + sp.ch - 1) - jn.first + 1;
         jn.slot = share.at(jn.first) == begin ? 0 : 1;
         jn.t = t0;
         jn.head = head0;
         jn.rows = rows;
-        jn.gdiv = geo.gdiv;
+        jn.gdiv = a.gdiv;
         join[c0 == 0] = jn;
       }
     }
-    __syncthreads();  // the stages are filled again
+    fence_async_smem();  // the copies that fill the stages again come behind these accesses
+    __syncthreads();
     w += c1 - c0;
     c0 = 0;
-    ++unit;
+    if (++ut == sp.per_h) {
+      ut = 0;
+      ++h;
+    }
   }
 }
 
@@ -774,7 +804,13 @@ __global__ void __launch_bounds__(256) k8_join_kernel(const K8Fwd a, const float
           }
         }
       }
-      if ((step == 1 || warp == 0) && lane < DV / 4) k8_finish(a, jn.t + row / jn.gdiv, head, 4 * lane, sink, top, sum, v);
+      if (step == 1 || warp == 0) {
+        const int t = jn.t + row / jn.gdiv;
+        float lse;
+        const float norm = k8_norm(sink, top, sum, &lse);
+        if (lane == 0) a.lse[(long long)t * a.Hq + head] = lse;
+        if (lane < DV / 4) k8_store(a, t, head, 4 * lane, norm, v);
+      }
       if (step == 8) __syncthreads();  // sl, so
     }
   }
@@ -783,13 +819,12 @@ __global__ void __launch_bounds__(256) k8_join_kernel(const K8Fwd a, const float
 // CTAs of the split kernel: all that the SMs hold at once, or as many as the longest
 // possible line has chunks.
 static int k8_split_ctas(const K8Fwd& a) {
-  const K8Geom g = k8_geom(a);
   const int occ = a.c.dqk + a.c.dv <= 128 ? 4 : (a.c.dqk <= 128 ? 3 : 2);
-  const long long units = ((long long)(a.c.T + g.tpt - 1) / g.tpt + (g.tpt > 1 ? min(a.c.B, a.c.T) : 0)) * g.hs * a.c.Hkv;
-  long long ch = g.sel_ch;
+  const long long units = ((long long)(a.c.T + a.tpt - 1) / a.tpt + (a.tpt > 1 ? min(a.c.B, a.c.T) : 0)) * a.hs * a.c.Hkv;
+  long long ch = a.sel_ch;
   if (!ch) {
     ch = ((long long)a.c.max_pages * a.c.ps + kK8Chunk - 1) / kK8Chunk;
-    if (a.win < (1 << 29)) ch = min(ch, (long long)(a.win + g.tpt + 15 + kK8Chunk - 1) / kK8Chunk);
+    if (a.win < (1 << 29)) ch = min(ch, (long long)(a.win + a.tpt + 15 + kK8Chunk - 1) / kK8Chunk);
   }
   return (int)min((long long)148 * occ, units * max(ch, 1ll));
 }
@@ -800,8 +835,17 @@ static cudaError_t split_t(const K8Fwd& a, void* ws, cudaStream_t st) {
   auto k = k8_split_kernel<DK, DV, ROWS, FMT>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (e != cudaSuccess) return e;
+  K8Maps maps;
+  memset(&maps, 0, sizeof(maps));
+  if (!ROWS) {
+    const uint64_t rows = (uint64_t)a.c.n_pages * a.c.ps, heads = a.c.Hkv;
+    if (!make_tmap_codes(&maps.k, a.c.k, rows, heads, DK, DK == 64 ? 64 : 128, 16) ||
+        !make_tmap_codes(&maps.v, a.c.v, rows, heads, DV, DV, 16) ||
+        (DK == 192 && !make_tmap_codes(&maps.k2, a.c.k + 128, rows, heads, 192, 64, 16)))
+      return cudaErrorInvalidValue;
+  }
   const int n = k8_split_ctas(a);
-  k<<<(unsigned)n, 128, P::kSmem, st>>>(a, static_cast<float*>(ws));
+  k<<<(unsigned)n, 128, P::kSmem, st>>>(a, maps, static_cast<float*>(ws));
   count_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess || n == 1) return e;
@@ -910,19 +954,30 @@ __global__ void __launch_bounds__(128) k8_row_kernel(K8Fwd a) {
 
 static bool k8_latent(const K8Fwd& a) { return a.c.dqk > 192; }
 
-size_t k8_fwd_workspace(const K8Fwd& a) {
+static void k8_geometry(K8Fwd& a) {
+  a.gdiv = a.G < 16 ? a.G : 16;
+  a.hs = (a.G + 15) / 16;
+  a.tpt = a.topk || a.G > 16 ? 1 : 16 / a.G;
+  a.sel_ch = a.topk ? (int)(((long long)a.topk * a.bs + kK8Chunk - 1) / kK8Chunk) : 0;
+  a.by_tpt = k8_div_of(a.tpt);
+  a.by_gdiv = k8_div_of(a.gdiv);
+}
+
+size_t k8_fwd_workspace(K8Fwd a) {
   if (k8_latent(a)) return 0;
+  k8_geometry(a);
   const int n = k8_split_ctas(a);
   return k8_parts_at(n) + (size_t)n * 2 * k8_part_floats(a.c.dv) * sizeof(float);
 }
 
-cudaError_t launch_kv8_fwd(const K8Fwd& a, void* ws, cudaStream_t st) {
+cudaError_t launch_kv8_fwd(K8Fwd a, void* ws, cudaStream_t st) {
   if (a.c.T == 0 || a.c.B == 0) return cudaSuccess;
   if (k8_latent(a)) {
     k8_row_kernel<<<dim3((unsigned)a.c.T, (unsigned)a.Hq), 128, 0, st>>>(a);
     count_launch();
     return cudaGetLastError();
   }
+  k8_geometry(a);
   if (a.c.dqk == 64) return split_d<64, 64>(a, ws, st);
   if (a.c.dqk == 128) return split_d<128, 128>(a, ws, st);
   return split_d<192, 128>(a, ws, st);

@@ -76,6 +76,9 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned
 // of box_rows x 64 columns, 128-byte swizzle, zero fill out of range.
 bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t row_stride_bytes,
                     uint32_t box_rows);
+// The same over [rows][heads][d] one-byte codes, boxes of box_rows x box_d of one head.
+bool make_tmap_codes(CUtensorMap* map, const void* base, uint64_t rows, uint64_t heads, uint64_t d, uint32_t box_d,
+                     uint32_t box_rows);
 
 // Returns false when no kernel is built for (dqk, dv, shared).
 bool kernels_built(int dqk, int dv, bool shared);
