@@ -15,37 +15,43 @@ bool k8_built(int dqk, int dv, bool shared) {
 }
 
 // ---------------------------------------------------------------------------
-// separate K and V, or any row of at most 192 columns: split over the rows
+// rows of up to 192 columns: split over the rows
 // ---------------------------------------------------------------------------
 // Work.  A unit is up to 16 query rows of one KV head: the G heads of 16 / G tokens
 // of a sequence, or 16 of a token's heads where G > 16, or the heads of one token where
-// each token selects its own blocks.  A unit's rows are cut into chunks of 64, and the
+// each token selects its own blocks.  A unit's rows are cut into chunks of 128, and the
 // chunks of all units lie on one line that is cut evenly over the CTAs, wherever a unit
 // begins or ends: ragged lengths balance by themselves.  A unit that lies inside one
 // CTA is finished there; the others leave (maximum, sum, O) of each part in the
 // workspace for k8_join_kernel.
-// A warp takes 16 rows of a chunk through a pipeline of its own (cp.async, no block
+// A warp takes 32 rows of a chunk per step (two halves of 16, each within one page and
+// one block, so with one scale) through a pipeline of its own (TMA boxes, no block
 // barrier), keeps its own running maximum, sum and O, and the four warps meet once per
-// unit.  Codes become halves in registers right before the MMA (exact): K straight from
-// 16-byte reads of its rows, with the head dimension permuted alike in Q; V through
-// transposed ldmatrix of byte pairs, two output columns per 16-bit element.
-// Scales.  Q is held as halves times a power of two per row (exact for bf16 but for
-// what lies 2^-30 below the row's largest).  V's scale goes into the exponent: with
-// w_j = s_j + log2 vs_j the products use p'_j = 2^(w_j - max w), and the sum gets
-// p'_j / vs_j.  So P needs one exponential, and its 11 bits sit where the products are
-// largest whatever the pages' scales are.  p' <= 2^15: the maximum is let grow by up to
-// 2^4 before O is rescaled, and is held at 2^11.
+// unit.
+// Codes become halves in registers right before the MMA (m16n8k16; exact): K from 16-byte
+// reads of its rows, with the head dimension permuted alike in Q; V through transposed
+// ldmatrix of byte pairs, two output columns per 16-bit element.  (The fp8 m16n8k32 on
+// the codes themselves, with Q and P as sums of e5m2 terms, measured 1.8 times slower:
+// 499 against 273 us on 645 k rows of 8 heads at 128 / 128.)
+// Scales.  Q is held times a power of two per row (what lies 2^-30 below the row's
+// largest is lost).  V's scale goes into the exponent: with w_j = s_j + log2 vs_j the
+// products use p'_j = 2^(w_j - max w), and the sum gets p'_j / vs_j.  So P needs one
+// exponential, and its 11 bits sit where the products are largest whatever the pages'
+// scales are.  p' <= 2^15: the maximum is let grow by up to 2^4 before O is rescaled,
+// and is held at 2^11.
 constexpr int kK8Warps = 4;
-constexpr int kK8Chunk = 16 * kK8Warps;
+constexpr int kK8Chunk = 32 * kK8Warps;
 constexpr float kK8Grow = 4.f, kK8Top = 11.f;
 
-template <int DK, int DV, bool ROWS>
+template <int DK, int DV, bool ROWS, int FMT>
 struct K8Split {
-  static constexpr int kData = 16 * (DK + DV);
-  static constexpr int kMeta = ROWS ? 192 : 16;  // scales and rows of a step
-  static constexpr int kStages = DK + DV <= 128 ? 6 : 4;
+  static constexpr int kData = 32 * (DK + DV);
+  static constexpr int kMeta = ROWS ? 384 : 32;  // rows and scales of a step
+  static constexpr int kStages = DK + DV <= 128 ? 3 : 2;
   static constexpr int kOcc = DK + DV <= 128 ? 4 : (DK <= 128 ? 3 : 2);
-  static constexpr int kMetaAt = kK8Warps * kStages * kData;
+  static constexpr int kQ = DK / 16 * 512;  // Q in the MMA's order: 16 bytes per lane and k step
+  static constexpr int kQAt = kK8Warps * kStages * kData;
+  static constexpr int kMetaAt = kQAt + kQ;
   static constexpr int kBarAt = kMetaAt + kK8Warps * kStages * kMeta;
   static constexpr int kSmem = kBarAt + kK8Warps * kStages * 8 + 1024;  // the swizzles want 1024-byte alignment
   static constexpr int kLd = DV + 16;  // O in shared memory: rows 16 banks apart
@@ -55,7 +61,7 @@ struct K8Maps {
   CUtensorMap k, k2, v;  // columns 0 .. 127 (or 63) of K, columns 128 .. 191, V
 };
 
-// Byte of 16-byte piece p of row r in a step's 16 rows, as the TMA swizzles lay them.
+// Byte of 16-byte piece p of row r in a half step's 16 rows, as the TMA swizzles lay them.
 template <int D>
 __device__ __forceinline__ int k8_at(int r, int p) {
   if (D == 64) return r * 64 + ((p ^ ((r >> 1) & 3)) << 4);
@@ -74,20 +80,26 @@ __device__ __forceinline__ float2 k8_two(uint32_t v, int f16) {
   return f16 ? __half22float2(*reinterpret_cast<const __half2*>(&v))
              : make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
+__device__ __forceinline__ uint32_t k8_halves(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t k8_hsub2(uint32_t x, uint32_t y) {
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// A word of four codes as halves: bytes (0, 1) and (2, 3).  e4m3 by conversion; int8 as 1024 +
+// (code + 128), which is the byte under 0x64, less 1152 (exact).
 template <int FMT>
-__device__ __forceinline__ void k8_pair(uint32_t w, uint32_t& lo, uint32_t& hi) {  // bytes (0, 1) and (2, 3)
+__device__ __forceinline__ void k8_pair(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if (FMT == kFmtE4M3) {
     asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
         : "=r"(lo), "=r"(hi)
         : "r"(w));
   } else {
-    // 1024 + (code + 128) as a half is the byte under 0x64; the subtraction is exact
     const uint32_t u = w ^ 0x80808080u;
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));
-    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), off), y = __hsub2(*reinterpret_cast<__half2*>(&b), off);
-    lo = *reinterpret_cast<const uint32_t*>(&x);
-    hi = *reinterpret_cast<const uint32_t*>(&y);
+    lo = k8_hsub2(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u);
+    hi = k8_hsub2(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
   }
 }
 template <int FMT>
@@ -96,18 +108,15 @@ __device__ __forceinline__ void k8_pair_t(uint32_t w, uint32_t& even, uint32_t& 
     k8_pair<FMT>(__byte_perm(w, 0, 0x3120), even, odd);
   } else {
     const uint32_t u = w ^ 0x80808080u;
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));
-    uint32_t a = __byte_perm(u, 0x64646464u, 0x4240), b = __byte_perm(u, 0x64646464u, 0x4341);
-    const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), off), y = __hsub2(*reinterpret_cast<__half2*>(&b), off);
-    even = *reinterpret_cast<const uint32_t*>(&x);
-    odd = *reinterpret_cast<const uint32_t*>(&y);
+    even = k8_hsub2(__byte_perm(u, 0x64646464u, 0x4240), 0x64806480u);
+    odd = k8_hsub2(__byte_perm(u, 0x64646464u, 0x4341), 0x64806480u);
   }
 }
-__device__ __forceinline__ void k8_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void k8_mma(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void k8_cp4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
@@ -134,13 +143,13 @@ __device__ __forceinline__ void k8_box(uint32_t dst, const CUtensorMap* map, int
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(head), "r"(row), "r"(bar)
       : "memory");
 }
-// 16 rows of which lane r holds the row of the cache (negative: zeros)
+// 16 rows of which lane (from + r) holds the row of the cache (negative: zeros)
 template <int D>
-__device__ __forceinline__ void k8_copy_rows(uint32_t dst, const uint8_t* src, int rs, int rr, int lane) {
+__device__ __forceinline__ void k8_copy_rows(uint32_t dst, const uint8_t* src, int rs, int rr, int from, int lane) {
 #pragma unroll
   for (int it = 0; it < D / 32; ++it) {
     const int i = it * 32 + lane, r = i / (D / 16), pc = i - r * (D / 16);
-    const int at = __shfl_sync(~0u, rr, r);
+    const int at = __shfl_sync(~0u, rr, from + r);
     cp_async16(dst + k8_at<D>(r, pc), src + (long long)(at >= 0 ? at : 0) * rs + pc * 16, at >= 0);
   }
 }
@@ -221,9 +230,9 @@ __device__ __forceinline__ K8Span k8_span(const K8Fwd& a, int b) {
 }
 
 template <int DK, int DV, bool ROWS, int FMT>
-__global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc)
+__global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
     k8_split_kernel(const __grid_constant__ K8Fwd a, const __grid_constant__ K8Maps maps, float* ws) {
-  using P = K8Split<DK, DV, ROWS>;
+  using P = K8Split<DK, DV, ROWS, FMT>;
   constexpr int S = P::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023);
@@ -232,6 +241,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc)
   __shared__ int found[4];        // that sequence, the head, the unit of the head, the chunk
   __shared__ K8Span found_span;
   __shared__ int dead_word;
+  __shared__ float q_scale[16];
   const K8Cache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, q4 = lane & 3;
   if (tid == 0) dead_word = 0;
@@ -306,6 +316,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc)
   sp = found_span;
 
   uint8_t* const wsm = smem + warp * S * P::kData;
+  uint32_t* const sq = reinterpret_cast<uint32_t*>(smem + P::kQAt);
   uint8_t* const wmeta = smem + P::kMetaAt + warp * S * P::kMeta;
   const uint32_t sbase = smem_u32(wsm), mbase = smem_u32(wmeta), bar0 = smem_u32(bars);
   uint32_t phases = 0;  // of this warp's barriers
@@ -333,26 +344,29 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc)
     if (a.topk && a.topk_len) slots = min(slots, max(0, __ldg(a.topk_len + iu)));
     const int* table = c.table + b * c.tstride;
 
-    // --- Q: this thread's rows gr and gr + 8; the loads here, the conversion behind the first copies
-    uint4 raw[2][DK / 32];
-    int ta[2], lo[2];
+    // --- Q: warp w brings rows 4 w .. 4 w + 3, 8 lanes a row; the loads here, the rest behind the first copies
+    constexpr int kQw = DK / 64;  // 16-byte pieces of a lane: piece qp + 8 i of the row
+    const int qrow = warp * 4 + (lane >> 3), qp = lane & 7;
+    uint4 raw[kQw];
+    {
+      const int tok = k8_quot(a.by_gdiv, qrow);
+      const char* src = static_cast<const char*>(a.q) +
+                        ((long long)(t0 + tok) * a.qstride + (long long)(head0 + qrow - tok * a.gdiv) * DK) * 2;
+#pragma unroll
+      for (int i = 0; i < kQw; ++i)
+        raw[i] = qrow < rows ? __ldg(reinterpret_cast<const uint4*>(src + (qp + 8 * i) * 16)) : make_uint4(0, 0, 0, 0);
+    }
+    int ta[2], lo[2];  // of this thread's rows gr and gr + 8
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int row = gr + 8 * r, tok = k8_quot(a.by_gdiv, row);
-      ta[r] = ta0 + min(tok, ntok - 1);
+      ta[r] = ta0 + min(k8_quot(a.by_gdiv, gr + 8 * r), ntok - 1);
       lo[r] = a.win >= ta[r] ? 0 : ta[r] - a.win;
-      const char* src = static_cast<const char*>(a.q) +
-                        ((long long)(t0 + tok) * a.qstride + (long long)(head0 + row - tok * a.gdiv) * DK) * 2;
-#pragma unroll
-      for (int i = 0; i < DK / 32; ++i)  // columns 64 * (i / 2) + 16 * q4 + 8 * (i % 2) ..
-        raw[r][i] = row < rows ? __ldg(reinterpret_cast<const uint4*>(src + (64 * (i >> 1) + 16 * q4 + 8 * (i & 1)) * 2))
-                               : make_uint4(0, 0, 0, 0);
     }
     const float sink = (tid >> 3) < rows ? k8_sink(a, head0 + k8_rem(a.by_gdiv, tid >> 3)) : -INFINITY;
 
-    // --- the steps of this warp: 16 rows of each chunk ----------------------------
+    // --- the steps of this warp: 32 rows of each chunk; lane x of 32 (ROWS) or of 2 resolves row (or half) x
     const int n_steps = c1 - c0;
-    const int p0 = c0 * kK8Chunk + warp * 16 + (ROWS ? (lane & 15) : 0);
+    const int p0 = c0 * kK8Chunk + warp * 32 + (ROWS ? lane : (lane & 1) * 16);
     auto fetch_idx = [&](int k) -> int {
       if (!a.topk) return 0;
       const int slot = k8_quot(a.by_bs, p0 + k * kK8Chunk);
@@ -382,28 +396,32 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc)
       const uint32_t dst = sbase + st * P::kData, meta = mbase + st * P::kMeta;
       int* im = reinterpret_cast<int*>(wmeta + st * P::kMeta);
       const int rr = row >= 0 ? page * c.ps + k8_rem(c.by_ps, row) : -1;  // row of the cache
-      const float* ks = c.ks + (long long)page * c.Hkv + h;
-      const float* vs = c.vs + (long long)page * c.Hkv + h;
+      const long long sc = (long long)page * c.Hkv + h;
       if (ROWS) {
-        if (lane < 16) {
+        im[lane] = row;
+        if (row >= 0) {
+          k8_cp4(meta + 128 + 4 * lane, c.ks + sc);
+          k8_cp4(meta + 256 + 4 * lane, c.vs + sc);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          k8_copy_rows<DK>(dst + x * 16 * DK, c.k + h * DK, krs, rr, 16 * x, lane);
+          k8_copy_rows<DV>(dst + 32 * DK + x * 16 * DV, c.v + h * DV, vrs, rr, 16 * x, lane);
+        }
+      } else {
+        const int both = (row >= 0) + __shfl_xor_sync(~0u, row >= 0, 1);
+        if (lane == 0 && both) mbar_arrive_tx(bars + st, both * 16 * (DK + DV));
+        __syncwarp();
+        if (lane < 2) {
           im[lane] = row;
           if (row >= 0) {
-            k8_cp4(meta + 64 + 4 * lane, ks);
-            k8_cp4(meta + 128 + 4 * lane, vs);
+            k8_cp4(meta + 8 + 4 * lane, c.ks + sc);
+            k8_cp4(meta + 16 + 4 * lane, c.vs + sc);
+            const uint32_t bar = bar0 + st * 8, kd = dst + lane * 16 * DK;
+            k8_box(kd, &maps.k, h, rr, bar);
+            if (DK == 192) k8_box(kd + 2048, &maps.k2, h, rr, bar);
+            k8_box(dst + 32 * DK + lane * 16 * DV, &maps.v, h, rr, bar);
           }
-        }
-        k8_copy_rows<DK>(dst, c.k + h * DK, krs, rr, lane);
-        k8_copy_rows<DV>(dst + 16 * DK, c.v + h * DV, vrs, rr, lane);
-      } else if (lane == 0) {
-        im[2] = row;
-        if (row >= 0) {
-          k8_cp4(meta, ks);
-          k8_cp4(meta + 4, vs);
-          const uint32_t bar = bar0 + st * 8;
-          mbar_arrive_tx(bars + st, P::kData);
-          k8_box(dst, &maps.k, h, rr, bar);
-          if (DK == 192) k8_box(dst + 2048, &maps.k2, h, rr, bar);
-          k8_box(dst + 16 * DK, &maps.v, h, rr, bar);
         }
       }
     };
@@ -417,45 +435,52 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc)
       pg[k] = fetch_page(rw[k]);
     }
 #pragma unroll
-    for (int k = 0; k < S - 1; ++k) {
+    for (int k = 0; k < S; ++k) {
       if (!dead) issue(k, rw[k], pg[k]);
       cp_async_commit();
     }
-    int next_row = rw[S - 1], next_page = pg[S - 1], next_x = xs[S];
+    int next_x = fetch_idx(S + 1), next_row = resolve(S, xs[S]), next_page = fetch_page(next_row);
 
-    // Q as halves times 2^(8 - E), E the exponent of the row's largest
-    uint32_t qa[DK / 16][4];
-    float fr[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    // Q as halves times 2^(14 - E), E the exponent of the row's largest, in the MMA's order
+    {
       float big = 0.f;
 #pragma unroll
-      for (int i = 0; i < DK / 32; ++i) {
-        const uint32_t v[4] = {raw[r][i].x, raw[r][i].y, raw[r][i].z, raw[r][i].w};
+      for (int i = 0; i < kQw; ++i) {
+        const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 f = k8_two(v[j], a.f16);
           big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
         }
       }
-      big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
-      big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
-      const int E = big > 0.f ? max((int)(__float_as_uint(big) >> 23) - 127, -110) : 8;
-      const float mul = __uint_as_float((uint32_t)(8 - E + 127) << 23);
-      fr[r] = a.scale_log2 * __uint_as_float((uint32_t)(E - 8 + 127) << 23);
 #pragma unroll
-      for (int i = 0; i < DK / 32; ++i) {
-        const uint32_t v[4] = {raw[r][i].x, raw[r][i].y, raw[r][i].z, raw[r][i].w};
+      for (int d = 1; d < 8; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
+      const int E = big > 0.f ? max((int)(__float_as_uint(big) >> 23) - 127, -110) : 14;
+      const float mul = __uint_as_float((uint32_t)(14 - E + 127) << 23);
+      if (qp == 0) q_scale[qrow] = a.scale_log2 * __uint_as_float((uint32_t)(E - 14 + 127) << 23);
+#pragma unroll
+      for (int i = 0; i < kQw; ++i) {
+        // columns 64 i + 8 qp .. + 7, that is 16 q4' + 8 x with q4' = qp / 2, x = qp % 2
+        const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint32_t hh[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 f = k8_two(v[j], a.f16);
-          const __half2 hh = __floats2half2_rn(f.x * mul, f.y * mul);
-          // column 64 ch + 16 q4 + 4 e + {0, 1 | 2, 3} is k {2 q4, + 1 | + 8, + 9} of step 4 ch + e
-          const int col = 8 * (i & 1) + 2 * j;
-          qa[(i >> 1) * 4 + (col >> 2)][r + 2 * ((col >> 1) & 1)] = *reinterpret_cast<const uint32_t*>(&hh);
+          hh[j] = k8_halves(f.x * mul, f.y * mul);
         }
+        // the lane that holds row qrow % 8 and columns q4' of the MMA; register r (+ 2 for the upper k)
+        const int to = (qrow & 7) * 4 + (qp >> 1), r = qrow >> 3;
+        // 4 columns are k 2 q4' + {0, 1 | 8, 9} of k step 4 i + 2 x + {0, 1}
+        uint32_t* dst = sq + ((4 * i + 2 * (qp & 1)) * 32 + to) * 4 + r;
+        dst[0] = hh[0];
+        dst[2] = hh[1];
+        dst[128] = hh[2];
+        dst[130] = hh[3];
       }
     }
+    __syncthreads();
+    const float fr[2] = {q_scale[gr], q_scale[gr + 8]};
+
     float o[DV / 16][2][4];
 #pragma unroll
     for (int i = 0; i < DV / 16; ++i)
@@ -466,196 +491,211 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS>::kOcc)
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float base[2] = {0.f, 0.f}, limit[2] = {-INFINITY, -INFINITY};  // m - kK8Top, and how far above it w may lie
 
-
-    int at = 0, fill = S - 1;  // stages of step k and of the one that is fetched
+    int at = 0;
     for (int k = 0; k < n_steps; ++k) {
-      k8_cp_wait<S - 2>();
+      k8_cp_wait<S - 1>();
       __syncwarp();
-      if (!dead) issue(fill, next_row, next_page);
-      cp_async_commit();
-      next_row = resolve(k + S, next_x);
-      next_page = fetch_page(next_row);
-      next_x = fetch_idx(k + S + 1);
-
       uint8_t* const st = wsm + at * P::kData;
-      const uint32_t sv = sbase + at * P::kData + 16 * DK;
+      uint8_t* const stv = st + 32 * DK;
+      const uint32_t sv = sbase + at * P::kData + 32 * DK;
       const int* im = reinterpret_cast<const int*>(wmeta + at * P::kMeta);
-      const int row0 = ROWS ? 0 : im[2], bit = at;
-      fill = at;
-      at = at + 1 == S ? 0 : at + 1;
-      if (!ROWS) {
-        if (row0 < 0 || dead) continue;
-        const uint32_t parity = (phases >> bit) & 1;
-        if (!__all_sync(~0u, mbar_try_wait(bars + bit, parity)) &&
-            !__all_sync(~0u, mbar_wait(bars + bit, parity, &dead_word, c.status))) {
+      int row0[2] = {ROWS ? 0 : im[0], ROWS ? 0 : im[1]};
+      bool any = !dead && (ROWS ? __any_sync(~0u, im[lane] >= 0) : row0[0] >= 0 || row0[1] >= 0);
+      if (!ROWS && any) {
+        const uint32_t parity = (phases >> at) & 1;
+        if (!__all_sync(~0u, mbar_try_wait(bars + at, parity)) &&
+            !__all_sync(~0u, mbar_wait(bars + at, parity, &dead_word, c.status))) {
           dead = 1;
-          continue;
+          any = false;
         }
-        phases ^= 1u << bit;
+        phases ^= (uint32_t)any << at;
       }
-      if (ROWS && __all_sync(~0u, im[lane & 15] < 0)) continue;
-
-      // scores of 16 rows
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      if (any) {
+        // --- scores of 32 rows: tiles 0, 1 of the first half, 2, 3 of the second ---
+        float s[4][4];
 #pragma unroll
-      for (int ch = 0; ch < DK / 64; ++ch)
+        for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+        const uint4* q = reinterpret_cast<const uint4*>(sq) + lane;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint4 kw = *reinterpret_cast<const uint4*>(st + k8_at<DK>(8 * j + k8_row<DK>(gr), ch * 4 + q4));
-          const uint32_t v[4] = {kw.x, kw.y, kw.z, kw.w};
+        for (int ch = 0; ch < DK / 64; ++ch) {
+          uint4 kw[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            kw[j] = *reinterpret_cast<const uint4*>(st + (j >> 1) * 16 * DK +
+                                                    k8_at<DK>(8 * (j & 1) + k8_row<DK>(gr), ch * 4 + q4));
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            uint32_t b0, b1;
-            k8_pair<FMT>(v[e], b0, b1);
-            k8_mma(s[j], qa[ch * 4 + e], b0, b1);
+            const uint4 qa = q[(4 * ch + e) * 32];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t b0, b1;
+              k8_pair<FMT>(e == 0 ? kw[j].x : e == 1 ? kw[j].y : e == 2 ? kw[j].z : kw[j].w, b0, b1);
+              k8_mma(s[j], qa, b0, b1);
+            }
           }
         }
 
-      // w = score + log2 of V's scale, less what the exponential's argument starts from;
-      // what a row does not see becomes -inf
-      float iv[2][2];
-      bool full = false;
-      if (!ROWS) {
-        const float ks = k8_scale(__int_as_float(im[0])), vs = k8_scale(__int_as_float(im[1]));
-        const float f0 = fr[0] * ks, f1 = fr[1] * ks, lv = k8_log2(vs), a0 = lv - base[0], a1 = lv - base[1];
-        iv[0][0] = k8_rcp(vs);
+        // --- w = score + log2 of V's scale, less what the exponential's argument starts from;
+        // what a row does not see becomes -inf ---
+        float iv[4][2];  // 1 / V's scale: per half, or per row
+        bool full = !ROWS;
+        if (!ROWS) {
+          const float* fm = reinterpret_cast<const float*>(im);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          s[j][0] = fmaf(s[j][0], f0, a0);
-          s[j][1] = fmaf(s[j][1], f0, a0);
-          s[j][2] = fmaf(s[j][2], f1, a1);
-          s[j][3] = fmaf(s[j][3], f1, a1);
-        }
-        full = row0 + 15 <= ta0 && row0 >= lo_last;
-        if (!full) {
+          for (int x = 0; x < 2; ++x) {
+            const float ks = k8_scale(fm[2 + x]), vs = k8_scale(fm[4 + x]);
+            const float f0 = fr[0] * ks, f1 = fr[1] * ks, lv = k8_log2(vs), a0 = lv - base[0], a1 = lv - base[1];
+            iv[x][0] = k8_rcp(vs);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+            for (int j = 2 * x; j < 2 * x + 2; ++j) {
+              s[j][0] = fmaf(s[j][0], f0, a0);
+              s[j][1] = fmaf(s[j][1], f0, a0);
+              s[j][2] = fmaf(s[j][2], f1, a1);
+              s[j][3] = fmaf(s[j][3], f1, a1);
+            }
+            full = full && row0[x] >= lo_last && row0[x] + 15 <= ta0;
+          }
+          if (!full) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int pos = row0 + 8 * j + k8_row<DK>(2 * q4 + (e & 1));
-              if (pos > ta[e >> 1] || pos < lo[e >> 1]) s[j][e] = -INFINITY;
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int pos = row0[j >> 1] + 8 * (j & 1) + k8_row<DK>(2 * q4 + (e & 1));
+                if (row0[j >> 1] < 0 || pos > ta[e >> 1] || pos < lo[e >> 1]) s[j][e] = -INFINITY;
+              }
+          }
+        } else {
+          const float* fm = reinterpret_cast<const float*>(im);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int col = 8 * j + k8_row<DK>(2 * q4 + e), pos = im[col];
+              const float ks = k8_scale(fm[32 + col]), vs = k8_scale(fm[64 + col]), lv = k8_log2(vs);
+              iv[j][e] = k8_rcp(vs);
+              s[j][e] = pos >= 0 && pos <= ta[0] && pos >= lo[0] ? fmaf(s[j][e], fr[0] * ks, lv - base[0]) : -INFINITY;
+              s[j][e + 2] =
+                  pos >= 0 && pos <= ta[1] && pos >= lo[1] ? fmaf(s[j][e + 2], fr[1] * ks, lv - base[1]) : -INFINITY;
             }
         }
-      } else {
-        const float* fm = reinterpret_cast<const float*>(im);
+        if (FMT == kFmtE4M3 && !full) {
+          // A NaN in a V row that some of the unit's rows do not see (a stale row of the page,
+          // a later token's): the product would carry it (0 * NaN) to all of them.  It is set
+          // into the rows that see it here, and out of the tile.  (A half without rows is
+          // whatever the stage held before.)
+          uint32_t nan = 0;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int col = 8 * j + k8_row<DK>(2 * q4 + e), pos = im[col];
-            const float ks = k8_scale(fm[16 + col]), vs = k8_scale(fm[32 + col]), lv = k8_log2(vs);
-            iv[j][e] = k8_rcp(vs);
-            s[j][e] = pos >= 0 && pos <= ta[0] && pos >= lo[0] ? fmaf(s[j][e], fr[0] * ks, lv - base[0]) : -INFINITY;
-            s[j][e + 2] =
-                pos >= 0 && pos <= ta[1] && pos >= lo[1] ? fmaf(s[j][e + 2], fr[1] * ks, lv - base[1]) : -INFINITY;
+          for (int i = 0; i < DV / 16; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(stv + (i * 32 + lane) * 16);
+            nan |= ((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) |
+                   ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u);
           }
-      }
-      if (FMT == kFmtE4M3 && !full) {
-        // A NaN in a V row that some of the unit's rows do not see (a stale row of the page,
-        // a later token's): the product would carry it (0 * NaN) to all of them.  It is set
-        // into the rows that see it here, and out of the tile.
-        uint32_t nan = 0;
-#pragma unroll
-        for (int i = 0; i < DV / 32; ++i) {
-          const uint4 v = *reinterpret_cast<const uint4*>(st + 16 * DK + (i * 32 + lane) * 16);
-          nan |= ((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) |
-                 ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u);
-        }
-        if (__any_sync(~0u, nan & 0x80808080u)) {
+          if (__any_sync(~0u, nan & 0x80808080u)) {
 #pragma unroll 1
-          for (int r = 0; r < 16; ++r) {
-            const int pos = ROWS ? im[r] : row0 + r;
-            const bool see[2] = {pos >= 0 && pos <= ta[0] && pos >= lo[0], pos >= 0 && pos <= ta[1] && pos >= lo[1]};
+            for (int r = 0; r < 32; ++r) {
+              const int first = r < 16 ? row0[0] : row0[1];
+              const int pos = ROWS ? im[r] : first < 0 ? -1 : first + (r & 15);
+              const bool see[2] = {pos >= 0 && pos <= ta[0] && pos >= lo[0], pos >= 0 && pos <= ta[1] && pos >= lo[1]};
 #pragma unroll
-            for (int pc = 0; pc < DV / 16; ++pc) {
-              const uint32_t v = *reinterpret_cast<const uint32_t*>(st + 16 * DK + k8_at<DV>(r, pc) + 4 * q4);
+              for (int pc = 0; pc < DV / 16; ++pc) {
+                const uint32_t v =
+                    *reinterpret_cast<const uint32_t*>(stv + (r >> 4) * 16 * DV + k8_at<DV>(r & 15, pc) + 4 * q4);
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                if (((v >> (8 * x)) & 0x7f) != 0x7f) continue;
-                if (see[0]) o[pc][x & 1][x >> 1] = __int_as_float(0x7fffffff);
-                if (see[1]) o[pc][x & 1][2 + (x >> 1)] = __int_as_float(0x7fffffff);
+                for (int x = 0; x < 4; ++x) {
+                  if (((v >> (8 * x)) & 0x7f) != 0x7f) continue;
+                  if (see[0]) o[pc][x & 1][x >> 1] = __int_as_float(0x7fffffff);
+                  if (see[1]) o[pc][x & 1][2 + (x >> 1)] = __int_as_float(0x7fffffff);
+                }
               }
             }
+            __syncwarp();
+            for (int i = lane; i < 8 * DV; i += 32) {
+              uint32_t* v = reinterpret_cast<uint32_t*>(stv) + i;
+              *v &= ~__vcmpeq4(*v & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            }
+            fence_async_smem();  // the next copy into this stage comes behind these writes
+            __syncwarp();
           }
-          __syncwarp();
-          for (int i = lane; i < 4 * DV; i += 32) {
-            uint32_t* v = reinterpret_cast<uint32_t*>(st + 16 * DK) + i;
-            *v &= ~__vcmpeq4(*v & 0x7f7f7f7fu, 0x7f7f7f7fu);
-          }
-          fence_async_smem();  // the next copy into this stage comes behind these writes
-          __syncwarp();
         }
-      }
 
-      // the running maximum; O is rescaled only when it grew by more than 2^kK8Grow
-      float mx[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-        mx[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-      if (__any_sync(~0u, mx[0] > limit[0] || mx[1] > limit[1])) {
+        // --- the running maximum; O is rescaled only when it grew by more than 2^kK8Grow ---
+        float mx[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 1));
-          mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 2));
-          const float mn = fmaxf(m[r], mx[r] + base[r]);
-          if (mn == -INFINITY) continue;
-          const float al = ex2_approx(m[r] - mn), shift = base[r] - (mn - kK8Top);
-          m[r] = mn;
-          base[r] = mn - kK8Top;
-          limit[r] = kK8Top + kK8Grow;
-          s[0][2 * r] += shift;
-          s[0][2 * r + 1] += shift;
-          s[1][2 * r] += shift;
-          s[1][2 * r + 1] += shift;
-          l[r] *= al;
+          mx[r] = fmaxf(s[0][2 * r], s[0][2 * r + 1]);
 #pragma unroll
-          for (int i = 0; i < DV / 16; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              o[i][e][2 * r] *= al;
-              o[i][e][2 * r + 1] *= al;
-            }
+          for (int j = 1; j < 4; ++j) mx[r] = fmaxf(mx[r], fmaxf(s[j][2 * r], s[j][2 * r + 1]));
         }
-      }
-      uint32_t pa[4];
-      {
+        if (__any_sync(~0u, mx[0] > limit[0] || mx[1] > limit[1])) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          s[j][0] = ex2_approx(s[j][0]);
-          s[j][1] = ex2_approx(s[j][1]);
-          s[j][2] = ex2_approx(s[j][2]);
-          s[j][3] = ex2_approx(s[j][3]);
-          const __half2 x = __floats2half2_rn(s[j][0], s[j][1]), y = __floats2half2_rn(s[j][2], s[j][3]);
-          pa[2 * j] = *reinterpret_cast<const uint32_t*>(&x);
-          pa[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&y);
+          for (int r = 0; r < 2; ++r) {
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 1));
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 2));
+            const float mn = fmaxf(m[r], mx[r] + base[r]);
+            if (mn == -INFINITY) continue;
+            const float al = ex2_approx(m[r] - mn), shift = base[r] - (mn - kK8Top);
+            m[r] = mn;
+            base[r] = mn - kK8Top;
+            limit[r] = kK8Top + kK8Grow;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              s[j][2 * r] += shift;
+              s[j][2 * r + 1] += shift;
+            }
+            l[r] *= al;
+#pragma unroll
+            for (int i = 0; i < DV / 16; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                o[i][e][2 * r] *= al;
+                o[i][e][2 * r + 1] *= al;
+              }
+          }
+        }
+        uint32_t ph[4][2];  // p' as halves: rows gr, gr + 8 of each tile
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[j][e] = ex2_approx(s[j][e]);
+          ph[j][0] = k8_halves(s[j][0], s[j][1]);
+          ph[j][1] = k8_halves(s[j][2], s[j][3]);
+          if (ROWS) {
+            l[0] = fmaf(s[j][0], iv[j][0], fmaf(s[j][1], iv[j][1], l[0]));
+            l[1] = fmaf(s[j][2], iv[j][0], fmaf(s[j][3], iv[j][1], l[1]));
+          }
         }
         if (!ROWS) {
-          l[0] = fmaf((s[0][0] + s[0][1]) + (s[1][0] + s[1][1]), iv[0][0], l[0]);
-          l[1] = fmaf((s[0][2] + s[0][3]) + (s[1][2] + s[1][3]), iv[0][0], l[1]);
-        } else {
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int x = 0; x < 2; ++x) {
+            l[0] = fmaf((s[2 * x][0] + s[2 * x][1]) + (s[2 * x + 1][0] + s[2 * x + 1][1]), iv[x][0], l[0]);
+            l[1] = fmaf((s[2 * x][2] + s[2 * x][3]) + (s[2 * x + 1][2] + s[2 * x + 1][3]), iv[x][0], l[1]);
+          }
+        }
+
+        // --- O += P V, a piece of 16 columns at a time ---
+        const uint4 pt[2] = {make_uint4(ph[0][0], ph[0][1], ph[1][0], ph[1][1]),
+                             make_uint4(ph[2][0], ph[2][1], ph[3][0], ph[3][1])};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              l[0] = fmaf(s[j][e], iv[j][e], l[0]);
-              l[1] = fmaf(s[j][e + 2], iv[j][e], l[1]);
-            }
+        for (int pc = 0; pc < DV / 16; ++pc) {
+          uint32_t v[4];  // tiles 0 .. 3
+          ldsm_x4_t(v, sv + (lane >> 4) * 16 * DV + k8_at<DV>(k8_row<DK>(lane & 7) + (lane & 8), pc));
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t e0, o0, e1, o1;
+            k8_pair_t<FMT>(v[2 * x], e0, o0);
+            k8_pair_t<FMT>(v[2 * x + 1], e1, o1);
+            k8_mma(o[pc][0], pt[x], e0, e1);
+            k8_mma(o[pc][1], pt[x], o0, o1);
+          }
         }
       }
-      // O += P V: two pieces of 16 columns at a time
-#pragma unroll
-      for (int pc = 0; pc < DV / 16; pc += 2) {
-        uint32_t v[4];
-        ldsm_x4_t(v, sv + k8_at<DV>(k8_row<DK>(lane & 7) + (lane & 8), pc + (lane >> 4)));
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint32_t e0, o0, e1, o1;
-          k8_pair_t<FMT>(v[2 * x], e0, o0);
-          k8_pair_t<FMT>(v[2 * x + 1], e1, o1);
-          k8_mma(o[pc + x][0], pa, e0, e1);
-          k8_mma(o[pc + x][1], pa, o0, o1);
-        }
-      }
+      __syncwarp();  // the stage has been read
+      if (!dead) issue(at, next_row, next_page);
+      cp_async_commit();
+      next_row = resolve(k + S + 1, next_x);
+      next_page = fetch_page(next_row);
+      next_x = fetch_idx(k + S + 2);
+      at = at + 1 == S ? 0 : at + 1;
     }
     k8_cp_wait<0>();
     if (dead) {
@@ -831,7 +871,7 @@ static int k8_split_ctas(const K8Fwd& a) {
 
 template <int DK, int DV, bool ROWS, int FMT>
 static cudaError_t split_t(const K8Fwd& a, void* ws, cudaStream_t st) {
-  using P = K8Split<DK, DV, ROWS>;
+  using P = K8Split<DK, DV, ROWS, FMT>;
   auto k = k8_split_kernel<DK, DV, ROWS, FMT>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (e != cudaSuccess) return e;
