@@ -51,9 +51,10 @@ struct K8Fwd {
   K8Cache c;
   int f16, Hq, G, bs, topk;
   K8Div by_bs;
-  // the units of query rows that the split kernel works on: tokens per unit, query rows of a
-  // token in a unit, units over a token's heads, and chunks of a unit that selects (0: every row)
-  int tpt, gdiv, hs, sel_ch;
+  // the units of query rows that the kernels work on: rows per chunk, query rows of a unit at
+  // most, tokens per unit, query rows of a token in a unit, units over a token's heads, and
+  // chunks of a unit that selects (0: every row)
+  int chunk, unit_rows, tpt, gdiv, hs, sel_ch;
   K8Div by_tpt, by_gdiv;
   int win;           // rows before the token's own that it sees (INT_MAX: all)
   float scale_log2;  // scale * log2(e)

@@ -47,10 +47,6 @@ __device__ __forceinline__ int k8_page(const K8Cache& c, int b, int row) {
   return -1;
 }
 
-__device__ __forceinline__ float k8_in(const void* p, long long i, int f16) {
-  return f16 ? __half2float(static_cast<const __half*>(p)[i]) : __bfloat162float(static_cast<const bf16*>(p)[i]);
-}
-
 // Two e4m3 codes (low byte first) -> two halves; exact.
 __device__ __forceinline__ uint32_t k8_e4m3x2(uint32_t two) {
   uint32_t r;

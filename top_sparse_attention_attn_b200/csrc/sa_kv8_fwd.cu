@@ -164,11 +164,14 @@ struct K8Join {
 };
 // The workspace: two K8Join per CTA (the unit in whose midst its share begins; the unit
 // that begins in its share and ends behind it), then two parts per CTA, slot 0 the one
-// that its share begins with: (maximum, sum) of 16 rows and O [16][DV].
+// that its share begins with: maxima and sums of a unit's rows (16, or 16 MT), and O [rows][DV].
 __host__ __device__ inline size_t k8_parts_at(int n_cta) {
   return ((size_t)n_cta * 2 * sizeof(K8Join) + 255) / 256 * 256;
 }
-__host__ __device__ inline size_t k8_part_floats(int dv) { return 32 + 16 * (size_t)dv; }
+__host__ __device__ inline size_t k8_part_floats(int rows, int dv) { return (size_t)rows * (2 + dv); }
+__device__ __forceinline__ float* k8_part(float* ws, int n_cta, int i, int rows, int dv) {
+  return reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + k8_parts_at(n_cta)) + i * k8_part_floats(rows, dv);
+}
 
 // n chunks shared evenly over CTAs: the first `rem` of them have one more.
 struct K8Share {
@@ -222,11 +225,117 @@ __device__ __forceinline__ K8Span k8_span(const K8Fwd& a, int b) {
   if (a.sel_ch) {
     r.ch = a.sel_ch;
   } else {
-    r.ch = max((r.s.L + kK8Chunk - 1) / kK8Chunk, 1);
+    r.ch = max((r.s.L + a.chunk - 1) / a.chunk, 1);
     // a window: from the step of 16 that its first row lies in
-    if (a.win < (1 << 29)) r.ch = min(r.ch, (a.win + a.tpt + 15 + kK8Chunk - 1) / kK8Chunk);
+    if (a.win < (1 << 29)) r.ch = min(r.ch, (a.win + a.tpt + 15 + a.chunk - 1) / a.chunk);
   }
   return r;
+}
+
+// Where a CTA stands on the line.
+struct K8Cursor {
+  long long w0, w1;  // its share
+  K8Share share;
+  long long seq_at;  // where the sequence begins
+  int b, h, ut, c0;  // sequence, KV head, unit of the head, first chunk of the unit
+  K8Span sp;
+};
+struct K8Found {
+  long long sum[8];
+  long long at;
+  int b, h, ut, c0;
+  K8Span sp;
+};
+// The line's length, this CTA's share and the unit that it begins in; false: it has none.
+template <int NT>
+__device__ __forceinline__ bool k8_begin(const K8Fwd& a, float* ws, int tid, K8Found& f, K8Cursor& cur) {
+  const int lane = tid & 31, warp = tid >> 5, B = a.c.B;
+  const int per = (B + NT - 1) / NT, b0 = min(tid * per, B), b1 = min(b0 + per, B);
+  long long mine = 0;
+  K8Span sp = {};
+  for (int b = b0; b < b1; ++b) {
+    sp = k8_span(a, b);
+    mine += (long long)sp.units * sp.ch;
+  }
+  long long inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(~0u, inc, d);
+    if (lane >= d) inc += x;
+  }
+  if (lane == 31) f.sum[warp] = inc;
+  __syncthreads();
+  long long W = 0, at = inc - mine;
+#pragma unroll
+  for (int x = 0; x < NT / 32; ++x) {
+    W += f.sum[x];
+    if (x < warp) at += f.sum[x];
+  }
+  const int n_cta = (int)min(W, (long long)gridDim.x);  // a share is empty only in CTAs behind these
+  if (tid < 2) (reinterpret_cast<K8Join*>(ws) + 2 * blockIdx.x)[tid].n = 0;
+  if (blockIdx.x >= n_cta) return false;
+  if (W <= 0x7fffffff) {
+    cur.share.base = (uint32_t)W / (uint32_t)n_cta;
+    cur.share.rem = (int)((uint32_t)W - (uint32_t)cur.share.base * (uint32_t)n_cta);
+  } else {
+    cur.share.base = W / n_cta;
+    cur.share.rem = (int)(W % n_cta);
+  }
+  cur.w0 = cur.share.at(blockIdx.x);
+  cur.w1 = cur.share.at(blockIdx.x + 1);
+  if (at <= cur.w0 && cur.w0 < at + mine) {
+    for (int b = b0;; ++b) {
+      if (b1 - b0 > 1) sp = k8_span(a, b);
+      const long long n = (long long)sp.units * sp.ch;
+      if (cur.w0 < at + n) {
+        const long long off = cur.w0 - at;
+        const int unit = off <= 0x7fffffff ? (int)((uint32_t)off / (uint32_t)sp.ch) : (int)(off / sp.ch);
+        f.at = at;
+        f.sp = sp;
+        f.b = b;
+        f.h = (uint32_t)unit / (uint32_t)sp.per_h;
+        f.ut = unit - f.h * sp.per_h;
+        f.c0 = (int)(off - (long long)unit * sp.ch);
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  cur.seq_at = f.at;
+  cur.sp = f.sp;
+  cur.b = f.b;
+  cur.h = f.h;
+  cur.ut = f.ut;
+  cur.c0 = f.c0;
+  return true;
+}
+__device__ __forceinline__ void k8_settle(const K8Fwd& a, K8Cursor& c) {  // to the next sequence with work
+  while (c.h >= a.c.Hkv || c.sp.units == 0) {
+    c.seq_at += (long long)c.sp.units * c.sp.ch;
+    c.sp = k8_span(a, ++c.b);
+    c.h = 0;
+  }
+}
+__device__ __forceinline__ void k8_next(K8Cursor& c) {
+  c.c0 = 0;
+  if (++c.ut == c.sp.per_h) {
+    c.ut = 0;
+    ++c.h;
+  }
+}
+// Notes that this CTA leaves a part of the unit at the cursor.
+__device__ __forceinline__ void k8_note(float* ws, const K8Cursor& c, int t, int head, int rows, int gdiv) {
+  const long long begin = c.seq_at + ((long long)c.h * c.sp.per_h + c.ut) * c.sp.ch;
+  K8Join jn;
+  jn.first = c.c0 == 0 ? (int)blockIdx.x : c.share.of(begin);
+  jn.n = c.share.of(begin + c.sp.ch - 1) - jn.first + 1;
+  jn.slot = c.share.at(jn.first) == begin ? 0 : 1;
+  jn.t = t;
+  jn.head = head;
+  jn.rows = rows;
+  jn.gdiv = gdiv;
+  (reinterpret_cast<K8Join*>(ws) + 2 * blockIdx.x)[c.c0 == 0] = jn;
 }
 
 template <int DK, int DV, bool ROWS, int FMT>
@@ -236,10 +345,6 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
   constexpr int S = P::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023);
-  __shared__ long long sum[4];
-  __shared__ long long found_at;  // where the share's first sequence begins on the line
-  __shared__ int found[4];        // that sequence, the head, the unit of the head, the chunk
-  __shared__ K8Span found_span;
   __shared__ int dead_word;
   __shared__ float q_scale[16];
   const K8Cache& c = a.c;
@@ -256,64 +361,10 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
   }
   pdl_trigger();  // the join waits for this kernel's end, but need not be launched after it
 
-  // the line's length, and the sequence that this CTA's share begins in
-  const int per = (c.B + 127) / 128, b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
-  long long mine = 0;
-  K8Span sp = {};
-  for (int b = b0; b < b1; ++b) {
-    sp = k8_span(a, b);
-    mine += (long long)sp.units * sp.ch;
-  }
-  long long inc = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long x = __shfl_up_sync(~0u, inc, d);
-    if (lane >= d) inc += x;
-  }
-  if (lane == 31) sum[warp] = inc;
-  __syncthreads();
-  const long long W = sum[0] + sum[1] + sum[2] + sum[3];
-  const int n_cta = (int)min(W, (long long)gridDim.x);  // a share is empty only in CTAs behind these
-  K8Join* const join = reinterpret_cast<K8Join*>(ws) + 2 * blockIdx.x;
-  if (tid < 2) join[tid].n = 0;
-  if (blockIdx.x >= n_cta) return;
-  K8Share share;
-  if (W <= 0x7fffffff) {
-    share.base = (uint32_t)W / (uint32_t)n_cta;
-    share.rem = (int)((uint32_t)W % (uint32_t)n_cta);
-  } else {
-    share.base = W / n_cta;
-    share.rem = (int)(W % n_cta);
-  }
-  const long long w0 = share.at(blockIdx.x), w1 = share.at(blockIdx.x + 1);
-  float* const parts = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + k8_parts_at(gridDim.x)) +
-                       2 * blockIdx.x * k8_part_floats(DV);
-  {
-    long long at = inc - mine;
-    for (int x = 0; x < warp; ++x) at += sum[x];
-    if (at <= w0 && w0 < at + mine) {
-      for (int b = b0;; ++b) {
-        if (b1 - b0 > 1) sp = k8_span(a, b);
-        const long long n = (long long)sp.units * sp.ch;
-        if (w0 < at + n) {
-          const long long off = w0 - at;
-          const int unit = off <= 0x7fffffff ? (int)((uint32_t)off / (uint32_t)sp.ch) : (int)(off / sp.ch);
-          found_at = at;
-          found_span = sp;
-          found[0] = b;
-          found[1] = (uint32_t)unit / (uint32_t)sp.per_h;
-          found[2] = unit - found[1] * sp.per_h;
-          found[3] = (int)(off - (long long)unit * sp.ch);
-          break;
-        }
-        at += n;
-      }
-    }
-    __syncthreads();
-  }
-  int b = found[0], h = found[1], ut = found[2], c0 = found[3];
-  long long seq_at = found_at;
-  sp = found_span;
+  __shared__ K8Found found;
+  K8Cursor cur;
+  if (!k8_begin<128>(a, ws, tid, found, cur)) return;
+  float* const parts = k8_part(ws, gridDim.x, 2 * blockIdx.x, 16, DV);
 
   uint8_t* const wsm = smem + warp * S * P::kData;
   uint32_t* const sq = reinterpret_cast<uint32_t*>(smem + P::kQAt);
@@ -323,13 +374,10 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
   int dead = 0;         // a wait gave up: no more copies, and NaN for a result
   const int krs = c.Hkv * DK, vrs = c.Hkv * DV;  // bytes from row to row of the cache
 
-  for (long long w = w0; w < w1;) {
-    while (h >= c.Hkv || sp.units == 0) {  // the next sequence with work
-      seq_at += (long long)sp.units * sp.ch;
-      sp = k8_span(a, ++b);
-      h = 0;
-    }
-    const int c1 = (int)min((long long)sp.ch, c0 + (w1 - w));
+  for (long long w = cur.w0; w < cur.w1;) {
+    k8_settle(a, cur);
+    const K8Span& sp = cur.sp;
+    const int b = cur.b, h = cur.h, ut = cur.ut, c0 = cur.c0, c1 = (int)min((long long)sp.ch, c0 + (cur.w1 - w));
     // a KV head's units lie together, a token's parts of the heads innermost
     const int tile = a.hs == 1 ? ut : ut / a.hs, hp = ut - tile * a.hs;
     const int t0 = sp.s.t0 + tile * a.tpt, ntok = min(a.tpt, sp.s.n - tile * a.tpt);
@@ -739,7 +787,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
       }
       const bool whole = c0 == 0 && c1 == sp.ch;
       // a part of a unit: slot 0 holds the one that this CTA's share begins with
-      float* part_out = parts + (w == w0 ? 0 : k8_part_floats(DV));
+      float* part_out = parts + (w == cur.w0 ? 0 : k8_part_floats(16, DV));
       if (row < rows) {
         const int tok = k8_quot(a.by_gdiv, row), t = t0 + tok, head = head0 + row - tok * a.gdiv;
         float lse, norm = 0.f;
@@ -765,51 +813,38 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
           part_out[16 + row] = total;
         }
       }
-      if (!whole && tid == 0) {
-        const long long begin = seq_at + ((long long)h * sp.per_h + ut) * sp.ch;
-        K8Join jn;
-        jn.first = c0 == 0 ? (int)blockIdx.x : share.of(begin);
-        jn.n = share.of(begin + sp.ch - 1) - jn.first + 1;
-        jn.slot = share.at(jn.first) == begin ? 0 : 1;
-        jn.t = t0;
-        jn.head = head0;
-        jn.rows = rows;
-        jn.gdiv = a.gdiv;
-        join[c0 == 0] = jn;
-      }
+      if (!whole && tid == 0) k8_note(ws, cur, t0, head0, rows, a.gdiv);
     }
     fence_async_smem();  // the copies that fill the stages again come behind these accesses
     __syncthreads();
     w += c1 - c0;
-    c0 = 0;
-    if (++ut == sp.per_h) {
-      ut = 0;
-      ++h;
-    }
+    k8_next(cur);
   }
 }
 
 // The units that span several CTAs.  The n blocks that held a part of a unit share its
 // rows: block x of them takes rows x, x + n, ...  Up to 8 parts, a warp sums a row's;
 // more, the 8 warps take an eighth of a row's parts each.  The order is fixed.
-template <int DV>
-__global__ void __launch_bounds__(256) k8_join_kernel(const K8Fwd a, const float* ws, int n_grid) {
+template <int R, int DV>
+__global__ void __launch_bounds__(256) k8_join_kernel(const K8Fwd a, float* ws, int n_grid) {
+  constexpr int NV = DV < 128 ? 1 : DV / 128, kLanes = DV < 128 ? DV / 4 : 32;  // float4 of a lane, lanes
   __shared__ float sl[8];
-  __shared__ float4 so[8][DV / 4];
+  __shared__ float4 so[8][NV * kLanes];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float* parts = reinterpret_cast<const float*>(reinterpret_cast<const char*>(ws) + k8_parts_at(n_grid));
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     const K8Join jn = reinterpret_cast<const K8Join*>(ws)[2 * blockIdx.x + which];
     if (jn.n == 0) continue;
     const int step = jn.n <= 8 ? 1 : 8, mine = blockIdx.x - jn.first;
+    auto part = [&](int x) { return k8_part(ws, n_grid, 2 * (jn.first + x) + (x ? 0 : jn.slot), R, DV); };
     for (int row = mine + (step == 1 ? warp * jn.n : 0); row < jn.rows; row += step == 1 ? 8 * jn.n : jn.n) {
-      auto part = [&](int x) { return parts + (2 * (jn.first + x) + (x ? 0 : jn.slot)) * k8_part_floats(DV); };
       const int head = jn.head + row % jn.gdiv;
       const float sink = k8_sink(a, head);
       float top = -INFINITY, sum = 0.f;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 v[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int x = lane; x < jn.n; x += 32) top = fmaxf(top, __ldcg(part(x) + row));
 #pragma unroll
       for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
@@ -817,29 +852,37 @@ __global__ void __launch_bounds__(256) k8_join_kernel(const K8Fwd a, const float
       for (int x = step == 1 ? 0 : warp; x < jn.n; x += step) {
         const float* p = part(x);
         const float f = top == -INFINITY ? 1.f : ex2_approx(__ldcg(p + row) - top);
-        sum = fmaf(__ldcg(p + 16 + row), f, sum);
-        if (lane < DV / 4) {
-          const float4 y = __ldcg(reinterpret_cast<const float4*>(p + 32 + row * DV) + lane);
-          v.x = fmaf(y.x, f, v.x);
-          v.y = fmaf(y.y, f, v.y);
-          v.z = fmaf(y.z, f, v.z);
-          v.w = fmaf(y.w, f, v.w);
+        sum = fmaf(__ldcg(p + R + row), f, sum);
+        if (lane < kLanes) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(p + 2 * R + row * DV) + lane + 32 * i);
+            v[i].x = fmaf(y.x, f, v[i].x);
+            v[i].y = fmaf(y.y, f, v[i].y);
+            v[i].z = fmaf(y.z, f, v[i].z);
+            v[i].w = fmaf(y.w, f, v[i].w);
+          }
         }
       }
       if (step == 8) {
         if (lane == 0) sl[warp] = sum;
-        if (lane < DV / 4) so[warp][lane] = v;
+        if (lane < kLanes)
+#pragma unroll
+          for (int i = 0; i < NV; ++i) so[warp][lane + 32 * i] = v[i];
         __syncthreads();
         if (warp == 0) {
-#pragma unroll
+#pragma unroll 1
           for (int x = 1; x < 8; ++x) {
             sum += sl[x];
-            if (lane < DV / 4) {
-              const float4 y = so[x][lane];
-              v.x += y.x;
-              v.y += y.y;
-              v.z += y.z;
-              v.w += y.w;
+            if (lane < kLanes) {
+#pragma unroll
+              for (int i = 0; i < NV; ++i) {
+                const float4 y = so[x][lane + 32 * i];
+                v[i].x += y.x;
+                v[i].y += y.y;
+                v[i].z += y.z;
+                v[i].w += y.w;
+              }
             }
           }
         }
@@ -849,22 +892,25 @@ __global__ void __launch_bounds__(256) k8_join_kernel(const K8Fwd a, const float
         float lse;
         const float norm = k8_norm(sink, top, sum, &lse);
         if (lane == 0) a.lse[(long long)t * a.Hq + head] = lse;
-        if (lane < DV / 4) k8_store(a, t, head, 4 * lane, norm, v);
+        if (lane < kLanes)
+#pragma unroll
+          for (int i = 0; i < NV; ++i) k8_store(a, t, head, 4 * (lane + 32 * i), norm, v[i]);
       }
       if (step == 8) __syncthreads();  // sl, so
     }
   }
 }
 
-// CTAs of the split kernel: all that the SMs hold at once, or as many as the longest
-// possible line has chunks.
-static int k8_split_ctas(const K8Fwd& a) {
-  const int occ = a.c.dqk + a.c.dv <= 128 ? 4 : (a.c.dqk <= 128 ? 3 : 2);
+static bool k8_latent(const K8Fwd& a) { return a.c.dqk > 192; }
+
+// CTAs: all that the SMs hold at once, or as many as the longest possible line has chunks.
+static int k8_ctas(const K8Fwd& a) {
+  const int occ = k8_latent(a) ? 1 : a.c.dqk + a.c.dv <= 128 ? 4 : (a.c.dqk <= 128 ? 3 : 2);
   const long long units = ((long long)(a.c.T + a.tpt - 1) / a.tpt + (a.tpt > 1 ? min(a.c.B, a.c.T) : 0)) * a.hs * a.c.Hkv;
   long long ch = a.sel_ch;
   if (!ch) {
-    ch = ((long long)a.c.max_pages * a.c.ps + kK8Chunk - 1) / kK8Chunk;
-    if (a.win < (1 << 29)) ch = min(ch, (long long)(a.win + a.tpt + 15 + kK8Chunk - 1) / kK8Chunk);
+    ch = ((long long)a.c.max_pages * a.c.ps + a.chunk - 1) / a.chunk;
+    if (a.win < (1 << 29)) ch = min(ch, (long long)(a.win + a.tpt + 15 + a.chunk - 1) / a.chunk);
   }
   return (int)min((long long)148 * occ, units * max(ch, 1ll));
 }
@@ -884,13 +930,13 @@ static cudaError_t split_t(const K8Fwd& a, void* ws, cudaStream_t st) {
         (DK == 192 && !make_tmap_codes(&maps.k2, a.c.k + 128, rows, heads, 192, 64, 16)))
       return cudaErrorInvalidValue;
   }
-  const int n = k8_split_ctas(a);
+  const int n = k8_ctas(a);
   k<<<(unsigned)n, 128, P::kSmem, st>>>(a, maps, static_cast<float*>(ws));
   count_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess || n == 1) return e;
   count_launch();
-  return launch_pdl(k8_join_kernel<DV>, (unsigned)n, 256, 0, st, a, (const float*)ws, n);
+  return launch_pdl(k8_join_kernel<16, DV>, (unsigned)n, 256, 0, st, a, static_cast<float*>(ws), n);
 }
 
 template <int DK, int DV>
@@ -902,122 +948,452 @@ static cudaError_t split_d(const K8Fwd& a, void* ws, cudaStream_t st) {
   return rows ? split_t<DK, DV, true, kFmtInt8>(a, ws, st) : split_t<DK, DV, false, kFmtInt8>(a, ws, st);
 }
 
-// One CTA per (token, query head): scores of 128 rows at a time, one per thread,
-// an online softmax, then each thread sums its output columns over the rows.
-__global__ void __launch_bounds__(128) k8_row_kernel(K8Fwd a) {
-  __shared__ float q[576], p[128], red[4];
-  __shared__ long long at[128];
-  __shared__ float vsc[128];
+// ---------------------------------------------------------------------------
+// a shared row of 576 columns, V its first 512
+// ---------------------------------------------------------------------------
+// A unit is one token and 16 MT of its heads (MT = 4 where there are more than 32); 64
+// rows per chunk and one CTA of 8 warps per SM, on the same line of chunks as above.  The
+// rows, selected one by one, are copied whole (cp.async, three stages), and serve as K and
+// V.  For the scores warp (mg, tg) takes the row tiles of its half of the heads against 16
+// of the rows (MT = 4), so that each code is converted twice; for O a warp takes all
+// heads against 64 of the columns.  P goes through shared memory between the two.  The
+// running maximum is shared by the CTA and looked at with the barrier that the stages
+// need anyway; it is exchanged only when some row's grew by more than 2^kK8Grow.
+// Bound: m16n8k16 issues (1024 products per cycle and SM), 64 rows x 64 heads in 4352 cycles.
+constexpr int kLatRows = 64, kLatDK = 576, kLatDV = 512;
+
+template <int MT>
+struct K8Lat {
+  static constexpr int kStages = 3;
+  static constexpr int kStage = kLatRows * kLatDK;
+  static constexpr int kQAt = kStages * kStage;
+  static constexpr int kQ = kLatDK / 16 * MT * 512;
+  static constexpr int kPAt = kQAt + kQ;
+  static constexpr int kP = MT * 16 * 128;
+  static constexpr int kMetaAt = kPAt + kP;
+  static constexpr int kMeta = kLatRows * 8;  // row, scale
+  static constexpr int kRedAt = kMetaAt + kStages * kMeta;
+  static constexpr int kSmem = kRedAt + 8 * MT * 16 * 4 + MT * 16 * 8;
+  // scores: warps along the heads and along the rows
+  static constexpr int kMG = MT == 1 ? 1 : 2, kTG = 8 / kMG, kMT = MT / kMG, kNT = kLatRows / 8 / kTG;
+};
+// piece p of row r (rows of 36 pieces, 64 bytes out of step with 128): 8 rows' same piece,
+// and two rows' four neighbouring pieces, on different banks
+__device__ __forceinline__ int lat_at(int r, int p) { return r * kLatDK + ((p ^ ((r >> 1) & 3)) << 4); }
+
+template <int MT, int FMT>
+__global__ void __launch_bounds__(256, 1) k8_latent_kernel(const __grid_constant__ K8Fwd a, float* ws) {
+  using P = K8Lat<MT>;
+  constexpr int S = P::kStages, R = MT * 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ K8Found found;
   const K8Cache& c = a.c;
-  const int t = blockIdx.x, hq = blockIdx.y, h = hq / a.G, tid = threadIdx.x;
-  const int b = k8_find(c, t);
-  const K8Seq s = k8_seq(c, b);
-  const int i = t - s.t0;
-  if (i < 0 || i >= s.n) return;
-  const int ta = s.first + i;
-  for (int d = tid; d < c.dqk; d += 128) q[d] = k8_in(a.q, t * a.qstride + (long long)hq * c.dqk + d, a.f16);
-  const int lo = a.win >= ta ? 0 : ta - a.win;
-  const long long unit = (long long)t * c.Hkv + h;
-  int slots = a.topk;
-  if (a.topk_len) slots = min(slots, max(0, __ldg(a.topk_len + unit)));
-  const int first = a.topk ? 0 : lo, n_rows = ta < 0 ? 0 : a.topk ? slots * a.bs : ta + 1;
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  const int n_o = (c.dv + 127) / 128;
-  for (int r0 = first; r0 < n_rows; r0 += 128) {
-    int row = r0 + tid;
-    bool see = row < n_rows;
-    if (see && a.topk) {
-      const int x = __ldg(a.idx + unit * a.topk + row / a.bs);
-      if (x >= 0 && (long long)x * a.bs >= s.L && c.status) atomicOr(c.status, kStatusIndexRange);
-      see = x >= 0 && (long long)x * a.bs < s.L;
-      row = see ? x * a.bs + row % a.bs : 0;
-    }
-    see = see && row >= lo && row <= ta;
-    const int page = see ? k8_page(c, b, row) : -1;
-    see = page >= 0;
-    float z = -INFINITY;
-    __syncthreads();
-    at[tid] = -1;
-    vsc[tid] = 0.f;
-    if (see) {
-      const long long rr = ((long long)page * c.ps + row % c.ps) * c.Hkv + h;
-      const uint8_t* k = c.k + rr * c.dqk;
-      float acc = 0.f;
-      for (int d = 0; d < c.dqk; ++d) acc = fmaf(q[d], k8_code(k[d], c.fmt), acc);
-      z = acc * k8_scale(c.ks[(long long)page * c.Hkv + h]) * a.scale_log2;
-      at[tid] = rr * (c.shared ? c.dqk : c.dv);
-      vsc[tid] = k8_scale((c.shared ? c.ks : c.vs)[(long long)page * c.Hkv + h]);
-    }
-    float mx = z;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, q4 = lane & 3;
+  const int mg = P::kMG == 1 ? 0 : warp & 1, tg = P::kMG == 1 ? warp : warp >> 1;
+  float* const red = reinterpret_cast<float*>(smem + P::kRedAt);  // [kTG][R]
+  float* const q_scale = red + 8 * R;                             // [R]
+  uint32_t* const sq = reinterpret_cast<uint32_t*>(smem + P::kQAt);
+  const uint32_t sp_at = smem_u32(smem + P::kPAt);
+  pdl_trigger();
+  K8Cursor cur;
+  if (!k8_begin<256>(a, ws, tid, found, cur)) return;
+  float* const parts = k8_part(ws, gridDim.x, 2 * blockIdx.x, R, kLatDV);
+  const int krs = c.Hkv * kLatDK;
+
+  for (long long w = cur.w0; w < cur.w1;) {
+    k8_settle(a, cur);
+    const K8Span& sp = cur.sp;
+    const int b = cur.b, h = cur.h, ut = cur.ut, c0 = cur.c0, c1 = (int)min((long long)sp.ch, c0 + (cur.w1 - w));
+    const int tile = a.hs == 1 ? ut : ut / a.hs, hp = ut - tile * a.hs;
+    const int t = sp.s.t0 + tile, ta = sp.s.first + tile;
+    const int head0 = h * a.G + hp * R, rows = min(R, a.G - hp * R);
+    const int lo = a.win >= ta ? 0 : ta - a.win, hi = min(ta + 1, sp.s.L), start = lo & ~15;
+    const long long iu = (long long)t * c.Hkv + h;
+    const int* idx = a.topk ? a.idx + iu * a.topk : nullptr;
+    int slots = a.topk;
+    if (a.topk && a.topk_len) slots = min(slots, max(0, __ldg(a.topk_len + iu)));
+    const int* table = c.table + b * c.tstride;
+
+    // warp w resolves and copies rows 8 w .. 8 w + 7 of a chunk (lane x: row x % 8)
+    const int n_steps = c1 - c0, p0 = c0 * kLatRows + warp * 8 + (lane & 7);
+    auto fetch_idx = [&](int k) -> int {
+      if (!a.topk) return 0;
+      const int slot = k8_quot(a.by_bs, p0 + k * kLatRows);
+      return k < n_steps && slot < slots ? __ldg(idx + slot) : -1;
+    };
+    auto resolve = [&](int k, int x) -> int {
+      if (k >= n_steps) return -1;
+      const int p = p0 + k * kLatRows;
+      int row = start + p;
+      if (a.topk) {
+        if (x < 0) return -1;
+        if ((long long)x * a.bs >= sp.s.L) {
+          if (c.status) atomicOr(c.status, kStatusIndexRange);
+          return -1;
+        }
+        row = x * a.bs + k8_rem(a.by_bs, p);
+      }
+      return row < hi && row >= lo ? row : -1;
+    };
+    auto fetch_page = [&](int row) -> int { return row >= 0 ? __ldg(table + k8_quot(c.by_ps, row)) : 0; };
+    auto issue = [&](int st, int row, int page) {
+      if (row >= 0 && (page < 0 || page >= c.n_pages)) {
+        if (c.status) atomicOr(c.status, kStatusIndexRange);
+        row = -1;
+      }
+      const int rr = row >= 0 ? page * c.ps + k8_rem(c.by_ps, row) : -1;
+      uint8_t* meta = smem + P::kMetaAt + st * P::kMeta;
+      if (lane < 8) {
+        reinterpret_cast<int*>(meta)[warp * 8 + lane] = row;
+        if (row >= 0) k8_cp4(smem_u32(meta) + 256 + 4 * (warp * 8 + lane), c.ks + (long long)page * c.Hkv + h);
+      }
+      const uint32_t dst = smem_u32(smem) + st * P::kStage;
+      const uint8_t* src = c.k + h * kLatDK;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
+      for (int it = 0; it < 9; ++it) {
+        const int i = it * 32 + lane, r = i / 36, pc = i - r * 36;
+        const int at = __shfl_sync(~0u, rr, r);
+        cp_async16(dst + lat_at(warp * 8 + r, pc), src + (long long)(at >= 0 ? at : 0) * krs + pc * 16, at >= 0);
+      }
+    };
+    int xs[S + 1], rw[S], pg[S];
+#pragma unroll
+    for (int k = 0; k <= S; ++k) xs[k] = fetch_idx(k);
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      rw[k] = resolve(k, xs[k]);
+      pg[k] = fetch_page(rw[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) {
+      issue(k, rw[k], pg[k]);
+      cp_async_commit();
+    }
+    int next_row = rw[S - 1], next_page = pg[S - 1], next_x = xs[S];
+
+    // Q, 8 lanes a row, as halves times 2^(14 - E) in the MMA's order
+#pragma unroll 1
+    for (int r0 = 0; r0 < R; r0 += 32) {
+      const int row = r0 + warp * 4 + (lane >> 3), qp = lane & 7;
+      if (R < 32 && row >= R) break;  // whole warps
+      const char* src = static_cast<const char*>(a.q) + ((long long)t * a.qstride + (long long)(head0 + row) * kLatDK) * 2;
+      uint4 raw[9];
+#pragma unroll
+      for (int i = 0; i < 9; ++i)
+        raw[i] = row < rows ? __ldg(reinterpret_cast<const uint4*>(src + (qp + 8 * i) * 16)) : make_uint4(0, 0, 0, 0);
+      float big = 0.f;
+#pragma unroll
+      for (int i = 0; i < 9; ++i) {
+        const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = k8_two(v[j], a.f16);
+          big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
+      const int E = big > 0.f ? max((int)(__float_as_uint(big) >> 23) - 127, -110) : 14;
+      const float mul = __uint_as_float((uint32_t)(14 - E + 127) << 23);
+      if (qp == 0) q_scale[row] = a.scale_log2 * __uint_as_float((uint32_t)(E - 14 + 127) << 23);
+      const int mt = row >> 4, to = (row & 7) * 4 + (qp >> 1), r = (row >> 3) & 1;
+#pragma unroll
+      for (int i = 0; i < 9; ++i) {
+        const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint32_t hh[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = k8_two(v[j], a.f16);
+          hh[j] = k8_halves(f.x * mul, f.y * mul);
+        }
+        uint32_t* dst = sq + (((4 * i + 2 * (qp & 1)) * MT + mt) * 32 + to) * 4 + r;
+        dst[0] = hh[0];
+        dst[2] = hh[1];
+        dst[MT * 128] = hh[2];
+        dst[MT * 128 + 2] = hh[3];
+      }
+    }
     __syncthreads();
-    mx = fmaxf(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), m);
-    const float base = mx == -INFINITY ? 0.f : mx, alpha = exp2f(m - base);
-    m = mx;
-    float pr = see ? exp2f(z - base) : 0.f;
-    p[tid] = pr;
+
+    float o[MT][4][2][4];  // heads x four pieces of 16 columns
+#pragma unroll
+    for (int x = 0; x < MT; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[x][i][e][j] = 0.f;
+    // of the score rows mg * kMT * 16 + 16 x + gr (+ 8)
+    float l[P::kMT][2], base[P::kMT][2], fr[P::kMT][2], limit = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < P::kMT; ++x)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        l[x][r] = base[x][r] = 0.f;
+        fr[x][r] = q_scale[(mg * P::kMT + x) * 16 + gr + 8 * r];
+      }
+    bool first = true;  // nothing seen yet: base is no maximum
+
+    int at = 0, fill = S - 1;
+    for (int k = 0; k < n_steps; ++k) {
+      k8_cp_wait<S - 2>();
+      __syncthreads();  // the chunk is there; the one before has been read (and P)
+      issue(fill, next_row, next_page);
+      cp_async_commit();
+      next_row = resolve(k + S, next_x);
+      next_page = fetch_page(next_row);
+      next_x = fetch_idx(k + S + 1);
+      const uint8_t* const st = smem + at * P::kStage;
+      const int* im = reinterpret_cast<const int*>(smem + P::kMetaAt + at * P::kMeta);
+      const float* fm = reinterpret_cast<const float*>(im) + 64;
+      fill = at;
+      at = at + 1 == S ? 0 : at + 1;
+
+      // --- scores ---
+      float s[P::kMT][P::kNT][4];
+#pragma unroll
+      for (int x = 0; x < P::kMT; ++x)
+#pragma unroll
+        for (int j = 0; j < P::kNT; ++j) s[x][j][0] = s[x][j][1] = s[x][j][2] = s[x][j][3] = 0.f;
+      const uint4* q = reinterpret_cast<const uint4*>(sq) + mg * P::kMT * 32 + lane;
+#pragma unroll 3
+      for (int ch = 0; ch < kLatDK / 64; ++ch) {
+        uint4 kw[P::kNT];
+#pragma unroll
+        for (int j = 0; j < P::kNT; ++j)
+          kw[j] = *reinterpret_cast<const uint4*>(st + lat_at((tg * P::kNT + j) * 8 + gr, ch * 4 + q4));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint4 qa[P::kMT];
+#pragma unroll
+          for (int x = 0; x < P::kMT; ++x) qa[x] = q[((4 * ch + e) * MT + x) * 32];
+#pragma unroll
+          for (int j = 0; j < P::kNT; ++j) {
+            uint32_t b0, b1;
+            k8_pair<FMT>(e == 0 ? kw[j].x : e == 1 ? kw[j].y : e == 2 ? kw[j].z : kw[j].w, b0, b1);
+#pragma unroll
+            for (int x = 0; x < P::kMT; ++x) k8_mma(s[x][j], qa[x], b0, b1);
+          }
+        }
+      }
+      float iv[P::kNT][2], mx[P::kMT][2];
+      bool grew = false;
+#pragma unroll
+      for (int x = 0; x < P::kMT; ++x) mx[x][0] = mx[x][1] = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < P::kNT; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int col = (tg * P::kNT + j) * 8 + 2 * q4 + e;
+          const bool see = im[col] >= 0;
+          const float ks = k8_scale(fm[col]), lv = k8_log2(ks);
+          iv[j][e] = k8_rcp(ks);
+#pragma unroll
+          for (int x = 0; x < P::kMT; ++x)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float& v = s[x][j][2 * r + e];
+              v = see ? fmaf(v, fr[x][r] * ks, lv - base[x][r]) : -INFINITY;
+              mx[x][r] = fmaxf(mx[x][r], v);
+            }
+        }
+#pragma unroll
+      for (int x = 0; x < P::kMT; ++x)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) grew = grew || mx[x][r] > limit;
+      if (__syncthreads_or(grew)) {
+        // the chunk's maxima over the warps that share the heads; those that grew move their base
+#pragma unroll
+        for (int x = 0; x < P::kMT; ++x)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float v = fmaxf(mx[x][r], __shfl_xor_sync(~0u, mx[x][r], 1));
+            v = fmaxf(v, __shfl_xor_sync(~0u, v, 2));
+            if (q4 == 0) red[tg * R + (mg * P::kMT + x) * 16 + gr + 8 * r] = v;
+          }
+        __syncthreads();
+        // a row's shift of its base (in units of log2): by how much its scores and O scale down
+        if (tid < R) {
+          float v = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < P::kTG; ++g) v = fmaxf(v, red[g * R + tid]);
+          // from the old base (0 before the first chunk with rows) to maximum - kK8Top
+          red[tid] = v > limit ? v - kK8Top : 0.f;
+          if (first && v == -INFINITY) red[tid] = 0.f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < P::kMT; ++x)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float d = red[(mg * P::kMT + x) * 16 + gr + 8 * r];
+            base[x][r] += d;
+            l[x][r] *= first ? 1.f : ex2_approx(-d);
+#pragma unroll
+            for (int j = 0; j < P::kNT; ++j) {
+              s[x][j][2 * r] -= d;
+              s[x][j][2 * r + 1] -= d;
+            }
+          }
+        if (!first) {
+#pragma unroll
+          for (int x = 0; x < MT; ++x)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float f = ex2_approx(-red[x * 16 + gr + 8 * r]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  o[x][i][e][2 * r] *= f;
+                  o[x][i][e][2 * r + 1] *= f;
+                }
+            }
+        }
+        first = false;
+        limit = kK8Top + kK8Grow;
+        __syncthreads();  // red is written again by the next exchange
+      }
+      // --- P ---
+#pragma unroll
+      for (int x = 0; x < P::kMT; ++x)
+#pragma unroll
+        for (int j = 0; j < P::kNT; ++j)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float p0v = ex2_approx(s[x][j][2 * r]), p1v = ex2_approx(s[x][j][2 * r + 1]);
+            l[x][r] = fmaf(p0v, iv[j][0], fmaf(p1v, iv[j][1], l[x][r]));
+            const int row = (mg * P::kMT + x) * 16 + gr + 8 * r, col = (tg * P::kNT + j) * 8 + 2 * q4;
+            *reinterpret_cast<uint32_t*>(smem + P::kPAt + row * 128 + (((col >> 3) ^ (row & 7)) << 4) + (col & 7) * 2) =
+                k8_halves(p0v, p1v);
+          }
+      __syncthreads();
+      // --- O += P V: this warp's 64 columns ---
+      const uint32_t sv = smem_u32(st);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        uint4 pa[MT];
+#pragma unroll
+        for (int x = 0; x < MT; ++x) {
+          const int row = x * 16 + (lane & 15), pc = kk * 2 + (lane >> 4);
+          uint32_t v[4];
+          ldsm_x4(v, sp_at + row * 128 + ((pc ^ (row & 7)) << 4));
+          pa[x] = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+#pragma unroll
+        for (int pc = 0; pc < 4; pc += 2) {
+          uint32_t v[4];
+          ldsm_x4_t(v, sv + lat_at(kk * 16 + (lane & 15), warp * 4 + pc + (lane >> 4)));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t e0, o0, e1, o1;
+            k8_pair_t<FMT>(v[2 * i], e0, o0);
+            k8_pair_t<FMT>(v[2 * i + 1], e1, o1);
+#pragma unroll
+            for (int x = 0; x < MT; ++x) {
+              k8_mma(o[x][pc + i][0], pa[x], e0, e1);
+              k8_mma(o[x][pc + i][1], pa[x], o0, o1);
+            }
+          }
+        }
+      }
+    }
+    k8_cp_wait<0>();
+
+    // --- sums over the warps that share the heads; out ---
     __syncthreads();
 #pragma unroll
-    for (int d = 16; d; d >>= 1) pr += __shfl_xor_sync(~0u, pr, d);
-    if ((tid & 31) == 0) red[tid >> 5] = pr;
+    for (int x = 0; x < P::kMT; ++x)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        l[x][r] += __shfl_xor_sync(~0u, l[x][r], 1);
+        l[x][r] += __shfl_xor_sync(~0u, l[x][r], 2);
+        const int row = (mg * P::kMT + x) * 16 + gr + 8 * r;
+        if (q4 == 0) red[tg * R + row] = l[x][r];
+        if (q4 == 0 && tg == 0) q_scale[row] = base[x][r];
+      }
     __syncthreads();
-    l = l * alpha + (red[0] + red[1] + red[2] + red[3]);
-    for (int j = 0; j < n_o; ++j) {
-      const int d = tid + j * 128;
-      if (d >= c.dv) break;
-      float acc = o[j] * alpha;
-      for (int r = 0; r < 128; ++r)
-        if (at[r] >= 0) acc = fmaf(p[r], vsc[r] * k8_code((c.shared ? c.k : c.v)[at[r] + d], c.fmt), acc);
-      o[j] = acc;
-    }
+    const bool whole = c0 == 0 && c1 == sp.ch;
+    float* part_out = parts + (w == cur.w0 ? 0 : k8_part_floats(R, kLatDV));
+#pragma unroll
+    for (int x = 0; x < MT; ++x)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = x * 16 + gr + 8 * r;
+        if (row >= rows) continue;
+        float total = 0.f;
+#pragma unroll
+        for (int g = 0; g < P::kTG; ++g) total += red[g * R + row];
+        const float m = first ? -INFINITY : q_scale[row] + kK8Top;
+        float lse, norm = 0.f;
+        if (whole) norm = k8_norm(k8_sink(a, head0 + row), m, total, &lse);
+        if (warp == 0 && q4 == 0) {
+          if (whole) {
+            a.lse[(long long)t * a.Hq + head0 + row] = lse;
+          } else {
+            part_out[row] = m;
+            part_out[R + row] = total;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int d = warp * 64 + i * 16 + 4 * q4;
+          const float4 v = make_float4(o[x][i][0][2 * r], o[x][i][1][2 * r], o[x][i][0][2 * r + 1], o[x][i][1][2 * r + 1]);
+          if (whole) k8_store(a, t, head0 + row, d, norm, v);
+          else *reinterpret_cast<float4*>(part_out + 2 * R + row * kLatDV + d) = v;
+        }
+      }
+    if (!whole && tid == 0) k8_note(ws, cur, t, head0, rows, a.gdiv);
+    __syncthreads();  // red, q_scale, the stages and Q are written again
+    w += c1 - c0;
+    k8_next(cur);
   }
-  if (a.sinks) {
-    const float sink = __ldg(a.sinks + hq) * 1.4426950408889634f, mx = fmaxf(m, sink);
-    const float base = mx == -INFINITY ? 0.f : mx, alpha = exp2f(m - base);
-    l = l * alpha + exp2f(sink - base);
-    for (int j = 0; j < n_o; ++j) o[j] *= alpha;
-    m = mx;
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  for (int j = 0; j < n_o; ++j) {
-    const int d = tid + j * 128;
-    if (d >= c.dv) break;
-    const float v = l == 0.f ? 0.f : o[j] * (l == l ? inv : l);
-    const long long e = ((long long)t * a.Hq + hq) * c.dv + d;
-    if (a.f16) static_cast<__half*>(a.o)[e] = __float2half_rn(v);
-    else static_cast<bf16*>(a.o)[e] = __float2bfloat16_rn(v);
-  }
-  if (tid == 0) a.lse[(long long)t * a.Hq + hq] = l == 0.f ? INFINITY : 0.6931471805599453f * (m + log2f(l));
 }
 
-static bool k8_latent(const K8Fwd& a) { return a.c.dqk > 192; }
+template <int MT, int FMT>
+static cudaError_t latent_t(const K8Fwd& a, void* ws, cudaStream_t st) {
+  using P = K8Lat<MT>;
+  auto k = k8_latent_kernel<MT, FMT>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  if (e != cudaSuccess) return e;
+  const int n = k8_ctas(a);
+  k<<<(unsigned)n, 256, P::kSmem, st>>>(a, static_cast<float*>(ws));
+  count_launch();
+  e = cudaGetLastError();
+  if (e != cudaSuccess || n == 1) return e;
+  count_launch();
+  return launch_pdl(k8_join_kernel<MT * 16, kLatDV>, (unsigned)n, 256, 0, st, a, static_cast<float*>(ws), n);
+}
+template <int FMT>
+static cudaError_t latent_f(const K8Fwd& a, void* ws, cudaStream_t st) {
+  if (a.unit_rows == 16) return latent_t<1, FMT>(a, ws, st);
+  if (a.unit_rows == 32) return latent_t<2, FMT>(a, ws, st);
+  return latent_t<4, FMT>(a, ws, st);
+}
 
 static void k8_geometry(K8Fwd& a) {
-  a.gdiv = a.G < 16 ? a.G : 16;
-  a.hs = (a.G + 15) / 16;
-  a.tpt = a.topk || a.G > 16 ? 1 : 16 / a.G;
-  a.sel_ch = a.topk ? (int)(((long long)a.topk * a.bs + kK8Chunk - 1) / kK8Chunk) : 0;
+  const bool lat = k8_latent(a);
+  a.chunk = lat ? kLatRows : kK8Chunk;
+  a.unit_rows = !lat ? 16 : a.G <= 16 ? 16 : a.G <= 32 ? 32 : 64;
+  a.gdiv = min(a.G, a.unit_rows);
+  a.hs = (a.G + a.unit_rows - 1) / a.unit_rows;
+  a.tpt = lat || a.topk || a.G > 16 ? 1 : 16 / a.G;
+  a.sel_ch = a.topk ? (int)(((long long)a.topk * a.bs + a.chunk - 1) / a.chunk) : 0;
   a.by_tpt = k8_div_of(a.tpt);
   a.by_gdiv = k8_div_of(a.gdiv);
 }
 
 size_t k8_fwd_workspace(K8Fwd a) {
-  if (k8_latent(a)) return 0;
   k8_geometry(a);
-  const int n = k8_split_ctas(a);
-  return k8_parts_at(n) + (size_t)n * 2 * k8_part_floats(a.c.dv) * sizeof(float);
+  const int n = k8_ctas(a);
+  return k8_parts_at(n) + (size_t)n * 2 * k8_part_floats(a.unit_rows, a.c.dv) * sizeof(float);
 }
 
 cudaError_t launch_kv8_fwd(K8Fwd a, void* ws, cudaStream_t st) {
   if (a.c.T == 0 || a.c.B == 0) return cudaSuccess;
-  if (k8_latent(a)) {
-    k8_row_kernel<<<dim3((unsigned)a.c.T, (unsigned)a.Hq), 128, 0, st>>>(a);
-    count_launch();
-    return cudaGetLastError();
-  }
   k8_geometry(a);
+  if (k8_latent(a)) return a.c.fmt == kFmtE4M3 ? latent_f<kFmtE4M3>(a, ws, st) : latent_f<kFmtInt8>(a, ws, st);
   if (a.c.dqk == 64) return split_d<64, 64>(a, ws, st);
   if (a.c.dqk == 128) return split_d<128, 128>(a, ws, st);
   return split_d<192, 128>(a, ws, st);
