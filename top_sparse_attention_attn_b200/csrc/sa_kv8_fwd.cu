@@ -919,7 +919,8 @@ template <int DK, int DV, bool ROWS, int FMT>
 static cudaError_t split_t(const K8Fwd& a, void* ws, cudaStream_t st) {
   using P = K8Split<DK, DV, ROWS, FMT>;
   auto k = k8_split_kernel<DK, DV, ROWS, FMT>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  static unsigned long long done = 0;
+  cudaError_t e = allow_smem(k, P::kSmem, done);
   if (e != cudaSuccess) return e;
   K8Maps maps;
   memset(&maps, 0, sizeof(maps));
@@ -1355,7 +1356,8 @@ template <int MT, int FMT>
 static cudaError_t latent_t(const K8Fwd& a, void* ws, cudaStream_t st) {
   using P = K8Lat<MT>;
   auto k = k8_latent_kernel<MT, FMT>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  static unsigned long long done = 0;
+  cudaError_t e = allow_smem(k, P::kSmem, done);
   if (e != cudaSuccess) return e;
   const int n = k8_ctas(a);
   k<<<(unsigned)n, 256, P::kSmem, st>>>(a, static_cast<float*>(ws));

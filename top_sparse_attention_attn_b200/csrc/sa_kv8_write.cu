@@ -116,7 +116,8 @@ __global__ void page_plan_kernel(PagePlan p) {
 cudaError_t launch_page_plan(const PagePlan& p, cudaStream_t st) {
   const unsigned block = p.B > 512 ? 1024 : 256;
   const size_t smem = (size_t)(p.B + 1) * 2 * sizeof(int);
-  cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static unsigned long long done = 0;
+  cudaError_t e = allow_smem(page_plan_kernel, (kPlanMaxBatch + 1) * 2 * (int)sizeof(int), done);
   if (e != cudaSuccess) return e;
   const int grid = min(148, max(1, (int)((p.T + (long long)block - 1) / block)));
   page_plan_kernel<<<grid, block, smem, st>>>(p);

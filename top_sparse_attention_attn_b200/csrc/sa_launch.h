@@ -72,6 +72,20 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Lets a kernel take `bytes` of dynamic shared memory on the current device, once per
+// device (the attribute is the device's): `done` holds a bit for each device served.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, unsigned long long& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (__atomic_load_n(&done, __ATOMIC_RELAXED) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) __atomic_fetch_or(&done, bit, __ATOMIC_RELAXED);
+  return e;
+}
+
 // TMA tensor map over a [rows][cols] bf16 matrix (row stride in bytes), boxes
 // of box_rows x 64 columns, 128-byte swizzle, zero fill out of range.
 bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t row_stride_bytes,
