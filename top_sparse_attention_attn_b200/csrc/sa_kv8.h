@@ -44,7 +44,8 @@ struct K8Write {
   int f16;
   const void *k, *v;
   long long kstride, vstride;
-  int window;  // tokens per CTA
+  int window;        // tokens per CTA
+  K8Div by_k, by_v;  // 8-element pieces of a K or V row
 };
 
 struct K8Fwd {

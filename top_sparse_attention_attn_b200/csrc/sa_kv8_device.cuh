@@ -35,18 +35,6 @@ __device__ __forceinline__ K8Seq k8_seq(const K8Cache& c, int b) {
   s.first = s.L - s.n;
   return s;
 }
-// The sequence of token t (the largest b with cu[b] <= t); the caller checks that t lies inside it.
-__device__ __forceinline__ int k8_find(const K8Cache& c, int t) { return c.cu ? find_batch(c.cu, c.B, t) : t / c.s_q; }
-
-// The page that holds a row of sequence b, or -1 (index bit raised) when the table
-// names none of the cache.  0 <= row < max_pages * ps.
-__device__ __forceinline__ int k8_page(const K8Cache& c, int b, int row) {
-  const int p = __ldg(c.table + b * c.tstride + row / c.ps);
-  if (p >= 0 && p < c.n_pages) return p;
-  if (c.status) atomicOr(c.status, kStatusIndexRange);
-  return -1;
-}
-
 // Two e4m3 codes (low byte first) -> two halves; exact.
 __device__ __forceinline__ uint32_t k8_e4m3x2(uint32_t two) {
   uint32_t r;

@@ -162,71 +162,134 @@ __device__ __forceinline__ void k8_unpack8(const uint4& r, float (&x)[8]) {
   }
 }
 
-// m new rows (x, `stride` apart) of one head to rows [off, off + m) of a page; 128
-// threads, which meet at named barrier `bar`.
-template <bool F16>
-__device__ __forceinline__ void k8_write_part(const char* x, long long stride, int m, int d, uint8_t* codes,
-                                              long long row_bytes, int off, float* scale, int fmt, int tid, int bar,
-                                              float* red) {
+// m new rows (x, `stride` apart) of head h to rows [off, off + m) of the page that `table`
+// names, none if it names none of the cache; NT threads, which meet at named barrier `bar`.
+// The rows are fetched before the table's answer is looked at.  A thread keeps its first kHold pieces of 8 elements
+// in registers between the maximum and the rounding, so that a page is read once; what a
+// larger page has beyond them is read again (from L1 or L2).
+template <bool F16, int NT>
+__device__ __forceinline__ void k8_write_part(const char* x, long long stride, int m, int d, const K8Div& by_per,
+                                              const K8Cache& cc, const int* table, uint8_t* cache, float* scales, int h,
+                                              int off, int tid, int bar, float* red) {
+  constexpr int kHold = NT == 512 ? 9 : NT == 128 ? 12 : 4;  // 64 rows of 576 or of 192; a few rows
+  const int page = __ldg(table), fmt = cc.fmt;
   const int per = d >> 3, n8 = m * per;
+  auto piece = [&](int i, int& r, int& c) {
+    r = k8_quot(by_per, i);
+    c = i - r * per;
+  };
+  uint4 hold[kHold];
+#pragma unroll
+  for (int j = 0; j < kHold; ++j) {
+    const int i = tid + j * NT;
+    int r, c;
+    piece(i, r, c);
+    if (i < n8) hold[j] = __ldg(reinterpret_cast<const uint4*>(x + r * stride * 2 + c * 16));
+  }
+  if (page < 0 || page >= cc.n_pages) {
+    if (cc.status) atomicOr(cc.status, kStatusIndexRange);
+    return;
+  }
+  float* const scale = scales + (long long)page * cc.Hkv + h;
+  const long long row_bytes = (long long)cc.Hkv * d;
+  uint8_t* const codes = cache + (long long)page * cc.ps * row_bytes + (long long)h * d;
+  const float before = off ? *scale : 0.f;
   float a = 0.f;
-  for (int i = tid; i < n8; i += 128) {
-    const int r = i / per, c = i - r * per;
+  auto most = [&](const uint4& w) {
     float v[8];
-    k8_unpack8<F16>(__ldg(reinterpret_cast<const uint4*>(x + r * stride * 2 + c * 16)), v);
+    k8_unpack8<F16>(w, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float s = fabsf(v[j]);
       a = fmaxf(a, s < INFINITY ? s : 0.f);  // infinities and NaN set no scale
     }
+  };
+#pragma unroll
+  for (int j = 0; j < kHold; ++j)
+    if (tid + j * NT < n8) most(hold[j]);
+  for (int i = tid + kHold * NT; i < n8; i += NT) {
+    int r, c;
+    piece(i, r, c);
+    most(__ldg(reinterpret_cast<const uint4*>(x + r * stride * 2 + c * 16)));
   }
 #pragma unroll
   for (int s = 16; s; s >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, s));
   if ((tid & 31) == 0) red[tid >> 5] = a;
-  const float before = off ? *scale : 0.f;
-  asm volatile("bar.sync %0, 128;\n" ::"r"(bar) : "memory");
-  a = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  asm volatile("bar.sync %0, %1;\n" ::"r"(bar), "n"(NT) : "memory");
+  a = red[0];
+#pragma unroll
+  for (int w = 1; w < NT / 32; ++w) a = fmaxf(a, red[w]);
   int e = k8_exp_for(a, fmt);
   if (off) e = max(e, k8_exp_at_least(before));
   const float after = k8_pow2(e), inv = k8_pow2(-e);  // x * 2^-e is x / s exactly
   if (off && before != after) {
     // rows that were there before: their codes in the new scale
     const float ratio = before / after;
-    const int p4 = d >> 2;
-    for (int i = tid; i < off * p4; i += 128) {
-      const int r = i / p4;
-      uint32_t* at = reinterpret_cast<uint32_t*>(codes + r * row_bytes + (i - r * p4) * 4);
-      const uint32_t w = *at;
-      float v[4];
+    for (int i = tid; i < off * per; i += NT) {
+      int r, c;
+      piece(i, r, c);
+      uint2* at = reinterpret_cast<uint2*>(codes + r * row_bytes + c * 8);
+      uint2 w = *at;
+      uint32_t* u = &w.x;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = k8_code((uint8_t)(w >> (8 * j)), fmt) * ratio;
-      *at = k8_round2(v[0], v[1], fmt) | (k8_round2(v[2], v[3], fmt) << 16);
+      for (int y = 0; y < 2; ++y) {
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = k8_code((uint8_t)(u[y] >> (8 * j)), fmt) * ratio;
+        u[y] = k8_round2(v[0], v[1], fmt) | (k8_round2(v[2], v[3], fmt) << 16);
+      }
+      *at = w;
     }
   }
-  for (int i = tid; i < n8; i += 128) {
-    const int r = i / per, c = i - r * per;
+  auto put = [&](int i, const uint4& w) {
+    int r, c;
+    piece(i, r, c);
     float v[8];
-    k8_unpack8<F16>(__ldg(reinterpret_cast<const uint4*>(x + r * stride * 2 + c * 16)), v);
+    k8_unpack8<F16>(w, v);
     uint2 o;
     o.x = k8_round2(v[0] * inv, v[1] * inv, fmt) | (k8_round2(v[2] * inv, v[3] * inv, fmt) << 16);
     o.y = k8_round2(v[4] * inv, v[5] * inv, fmt) | (k8_round2(v[6] * inv, v[7] * inv, fmt) << 16);
     *reinterpret_cast<uint2*>(codes + (off + r) * row_bytes + c * 8) = o;
+  };
+#pragma unroll
+  for (int j = 0; j < kHold; ++j)
+    if (tid + j * NT < n8) put(tid + j * NT, hold[j]);
+  for (int i = tid + kHold * NT; i < n8; i += NT) {
+    int r, c;
+    piece(i, r, c);
+    put(i, __ldg(reinterpret_cast<const uint4*>(x + r * stride * 2 + c * 16)));
   }
-  asm volatile("bar.sync %0, 128;\n" ::"r"(bar) : "memory");  // red[] and the old scale have been read
+  asm volatile("bar.sync %0, %1;\n" ::"r"(bar), "n"(NT) : "memory");  // red[] and the old scale have been read
   if (tid == 0) *scale = after;
+}
+
+// The sequence of token t, by a whole warp: a 32-way search of the offsets.
+__device__ __forceinline__ int k8_find_warp(const K8Cache& c, int t, int lane) {
+  if (!c.cu) return t / c.s_q;
+  int lo = 0, n = c.B;
+  while (n > 1) {
+    const int step = (n + 31) >> 5, at = lane * step;
+    const int below = __popc(__ballot_sync(~0u, at < n && __ldg(c.cu + lo + at) <= t));
+    const int k = max(below - 1, 0);
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
 }
 
 // One CTA per (window of tokens, head): it takes the page runs that begin in its
 // window (a run is the new rows of one page; a page's runs never split over CTAs, so
-// scale and codes have one writer).  Threads 0-127 write K and 128-255 V.
-template <bool F16>
-__global__ void __launch_bounds__(256) kv8_write_kernel(K8Write a) {
-  __shared__ float red[2][4];
+// scale and codes have one writer).  NT threads write K and as many V.  Bound by the
+// bytes for prompts (2 in, 1 out per element), by the chain offsets -> length -> table ->
+// scale for a row per request.
+template <bool F16, int NT, bool SHARED>
+__global__ void __launch_bounds__(SHARED ? NT : 2 * NT, NT == 512 ? 1 : NT == 128 ? 3 : 8) kv8_write_kernel(const __grid_constant__ K8Write a) {
+  __shared__ float red[2][NT / 32];
   const K8Cache& c = a.c;
-  const int h = blockIdx.y, half = threadIdx.x >> 7, tid = threadIdx.x & 127;
+  const int h = blockIdx.y, half = SHARED ? 0 : threadIdx.x / NT, tid = SHARED ? threadIdx.x : threadIdx.x % NT;
   int t = blockIdx.x * a.window;
   const int t_end = min(t + a.window, c.T);
-  int b = k8_find(c, t);
+  int b = k8_find_warp(c, t, threadIdx.x & 31);
   K8Seq s = k8_seq(c, b);
   while (t < t_end) {
     while (t >= s.t0 + s.n) {  // behind this sequence (or behind an empty one)
@@ -242,35 +305,44 @@ __global__ void __launch_bounds__(256) kv8_write_kernel(K8Write a) {
       t -= pos;
       continue;
     }
-    const int j = pos / c.ps, off = pos - j * c.ps, m = min(c.ps - off, s.n - i);
+    const int j = k8_quot(c.by_ps, pos), off = pos - j * c.ps, m = min(c.ps - off, s.n - i);
     const bool starts = i == 0 || off == 0 || pos == 0;
     if (starts) {
-      const int page = k8_page(c, b, pos);
-      if (page >= 0) {
-        const long long row = ((long long)page * c.ps * c.Hkv + h);
-        const int d = half ? c.dv : c.dqk;
-        const char* x = half ? static_cast<const char*>(a.v) + (t * a.vstride + (long long)h * d) * 2
-                             : static_cast<const char*>(a.k) + (t * a.kstride + (long long)h * d) * 2;
-        if (!half || !c.shared)
-          k8_write_part<F16>(x, half ? a.vstride : a.kstride, m, d, (half ? c.v : c.k) + row * d,
-                             (long long)c.Hkv * d, off, (half ? c.vs : c.ks) + (long long)page * c.Hkv + h, c.fmt, tid,
-                             1 + half, red[half]);
-      }
+      const int d = half ? c.dv : c.dqk;
+      const char* x = half ? static_cast<const char*>(a.v) + (t * a.vstride + (long long)h * d) * 2
+                           : static_cast<const char*>(a.k) + (t * a.kstride + (long long)h * d) * 2;
+      k8_write_part<F16, NT>(x, half ? a.vstride : a.kstride, m, d, half ? a.by_v : a.by_k, c, c.table + b * c.tstride + j,
+                             half ? c.v : c.k, half ? c.vs : c.ks, h, off, tid, 1 + half, red[half]);
     }
     t += m;
   }
 }
 
+template <int NT, bool SHARED>
+static void write_t(const K8Write& a, dim3 grid, cudaStream_t st) {
+  const unsigned block = SHARED ? NT : 2 * NT;
+  if (a.f16) kv8_write_kernel<true, NT, SHARED><<<grid, block, 0, st>>>(a);
+  else kv8_write_kernel<false, NT, SHARED><<<grid, block, 0, st>>>(a);
+}
+
 cudaError_t launch_kv8_write(K8Write a, cudaStream_t st) {
   if (a.c.T == 0 || a.c.B == 0) return cudaSuccess;
-  // about 16 CTAs per SM: a window of one token while the tokens are few (each may begin a page run)
+  // threads for a page's rows where the requests bring many, for a few rows otherwise; about
+  // as many CTAs as the SMs hold then, each with a run or so (a CTA per 18 tokens, most of
+  // which found no run, took 31 us where this takes 17: 10 k tokens, 4 heads of 192 / 128)
+  const bool many = a.c.T >= 8ll * a.c.B;
   const long long items = (long long)a.c.T * a.c.Hkv;
-  a.window = (int)((items + 148 * 16 - 1) / (148 * 16));
-  if (a.window < 1) a.window = 1;
+  a.window = (int)max(1ll, items / (148 * (many ? 4 : 16)));
   const dim3 grid((unsigned)((a.c.T + a.window - 1) / a.window), (unsigned)a.c.Hkv);
-  const unsigned block = a.c.shared ? 128 : 256;
-  if (a.f16) kv8_write_kernel<true><<<grid, block, 0, st>>>(a);
-  else kv8_write_kernel<false><<<grid, block, 0, st>>>(a);
+  a.by_k = k8_div_of(a.c.dqk / 8);
+  a.by_v = k8_div_of(a.c.dv / 8);
+  if (a.c.shared) {
+    if (many) write_t<512, true>(a, grid, st);
+    else write_t<64, true>(a, grid, st);
+  } else {
+    if (many) write_t<128, false>(a, grid, st);
+    else write_t<32, false>(a, grid, st);
+  }
   count_launch();
   return cudaGetLastError();
 }
