@@ -1,7 +1,8 @@
-"""Compile the CUDA sources of this package into libsparse_attn.so (in-tree).
+"""Compile the CUDA sources of this package into libsparse_attn.so (in-tree), and
+the CPython module that kv8.py calls it through.
 
-nvcc cross-compiles for sm_100a without a GPU; the shared library lands next
-to this file, where the ctypes binding loads it.
+nvcc cross-compiles for sm_100a without a GPU; the shared libraries land next
+to this file, where the bindings load them.
 """
 
 from __future__ import annotations
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -19,6 +21,10 @@ LIB = os.path.join(HERE, "libsparse_attn.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]
+
+
+EXT_SRC = os.path.join(CSRC, "ext", "kv8_ext.cpp")
+EXT = os.path.join(HERE, "_kv8_ext.so")
 
 
 def nvcc() -> str:
@@ -50,19 +56,43 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if force or _stale(obj, src):
             jobs.append([nvcc(), *ARCH, *FLAGS, "-c", src, "-o", obj])
 
-    def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
-        return r.stdout + r.stderr
-
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, len(jobs))) as ex:
-        for out in ex.map(run, jobs):
+    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, len(jobs) + 1)) as ex:
+        ext_obj = os.path.join(BUILD, "kv8_ext.o")
+        ext_stale = force or _stale(ext_obj, EXT_SRC)
+        ext = ex.submit(_run, _ext_compile(ext_obj)) if ext_stale else None
+        for out in ex.map(_run, jobs):
             if verbose and out.strip():
                 print(out)
+        if ext:
+            ext.result()
     if jobs or not os.path.exists(LIB):
-        run([nvcc(), *ARCH, "-shared", "-o", LIB, *objs, "-lcudart"])
+        _run([nvcc(), *ARCH, "-shared", "-o", LIB, *objs, "-lcudart"])
+    if ext_stale or not os.path.exists(EXT):
+        _run(_ext_link(ext_obj))
     return LIB
+
+
+def _run(cmd):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+    return r.stdout + r.stderr
+
+
+def _ext_compile(obj: str) -> list:
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+            "-isystem", sysconfig.get_paths()["include"], "-c", EXT_SRC, "-o", obj]
+
+
+def _ext_link(obj: str) -> list:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++", "-shared", "-o", EXT, obj, "-L" + HERE, "-l:libsparse_attn.so", "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
 
 
 if __name__ == "__main__":
