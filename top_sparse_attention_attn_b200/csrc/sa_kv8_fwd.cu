@@ -43,19 +43,32 @@ constexpr int kK8Warps = 4;
 constexpr int kK8Chunk = 32 * kK8Warps;
 constexpr float kK8Grow = 4.f, kK8Top = 11.f;
 
+// A unit, or a share's part of it, as its warps know it.
+struct alignas(16) K8Unit {
+  const int* idx;    // the token's indices (where it selects)
+  const int* table;  // the sequence's pages
+  long long begin;   // of the whole unit on the line
+  int slots, L;      // usable indices; rows of the sequence
+  int start, lo, hi; // the unit's first step, and the rows that any of its tokens sees
+  int h, t0, ntok, ta0, head0, rows;  // KV head, first token, tokens, its row, first query head, query rows
+  int c0, c1, ch;    // chunks of this part, and of the unit
+};
+
 template <int DK, int DV, bool ROWS, int FMT>
 struct K8Split {
   static constexpr int kData = 32 * (DK + DV);
   static constexpr int kMeta = ROWS ? 384 : 32;  // rows and scales of a step
   static constexpr int kStages = DK + DV <= 128 ? 3 : 2;
   static constexpr int kOcc = DK + DV <= 128 ? 4 : (DK <= 128 ? 3 : 2);
+  static constexpr int kRing = 8;         // units a warp may be ahead: kStages + 2 steps, and one in hand
   static constexpr int kQ = DK / 16 * 512;  // Q in the MMA's order: 16 bytes per lane and k step
   static constexpr int kQAt = kK8Warps * kStages * kData;
   static constexpr int kMetaAt = kQAt + kQ;
-  static constexpr int kBarAt = kMetaAt + kK8Warps * kStages * kMeta;
+  static constexpr int kUnitAt = kMetaAt + kK8Warps * kStages * kMeta;
+  static constexpr int kBarAt = kUnitAt + kK8Warps * kRing * (int)sizeof(K8Unit);
   static constexpr int kSmem = kBarAt + kK8Warps * kStages * 8 + 1024;  // the swizzles want 1024-byte alignment
-  static constexpr int kLd = DV + 16;  // O in shared memory: rows 16 banks apart
-  static_assert(16 * kLd * 4 + 128 <= kStages * kData, "a warp's result must fit in its stages");
+  static_assert(16 * DV * 4 <= kData, "a warp's O must fit in a stage");
+  static_assert(kStages + 3 <= kRing, "");
 };
 struct K8Maps {
   CUtensorMap k, k2, v;  // columns 0 .. 127 (or 63) of K, columns 128 .. 191, V
@@ -324,18 +337,49 @@ __device__ __forceinline__ void k8_next(K8Cursor& c) {
     ++c.h;
   }
 }
-// Notes that this CTA leaves a part of the unit at the cursor.
-__device__ __forceinline__ void k8_note(float* ws, const K8Cursor& c, int t, int head, int rows, int gdiv) {
-  const long long begin = c.seq_at + ((long long)c.h * c.sp.per_h + c.ut) * c.sp.ch;
+// Notes that this CTA leaves a part of a unit of `ch` chunks that begins at `begin`; c0: the part's first.
+__device__ __forceinline__ void k8_note(float* ws, const K8Share& share, long long begin, int c0, int ch, int t, int head,
+                                        int rows, int gdiv) {
   K8Join jn;
-  jn.first = c.c0 == 0 ? (int)blockIdx.x : c.share.of(begin);
-  jn.n = c.share.of(begin + c.sp.ch - 1) - jn.first + 1;
-  jn.slot = c.share.at(jn.first) == begin ? 0 : 1;
+  jn.first = c0 == 0 ? (int)blockIdx.x : share.of(begin);
+  jn.n = share.of(begin + ch - 1) - jn.first + 1;
+  jn.slot = share.at(jn.first) == begin ? 0 : 1;
   jn.t = t;
   jn.head = head;
   jn.rows = rows;
   jn.gdiv = gdiv;
-  (reinterpret_cast<K8Join*>(ws) + 2 * blockIdx.x)[c.c0 == 0] = jn;
+  (reinterpret_cast<K8Join*>(ws) + 2 * blockIdx.x)[c0 == 0] = jn;
+}
+// The unit at the cursor, which moves on; left: chunks left of the share.
+__device__ __forceinline__ K8Unit k8_take(const K8Fwd& a, K8Cursor& cur) {
+  k8_settle(a, cur);
+  const K8Span& sp = cur.sp;
+  K8Unit u;
+  u.h = cur.h;
+  u.c0 = cur.c0;
+  u.ch = sp.ch;
+  u.c1 = (int)min((long long)sp.ch, cur.c0 + (cur.w1 - cur.w0));
+  u.begin = cur.seq_at + ((long long)cur.h * sp.per_h + cur.ut) * sp.ch;
+  // a KV head's units lie together, a token's parts of the heads innermost
+  const int tile = a.hs == 1 ? cur.ut : cur.ut / a.hs, hp = cur.ut - tile * a.hs;
+  u.t0 = sp.s.t0 + tile * a.tpt;
+  u.ntok = min(a.tpt, sp.s.n - tile * a.tpt);
+  u.head0 = cur.h * a.G + hp * a.unit_rows;
+  u.rows = a.hs > 1 ? min(a.unit_rows, a.G - hp * a.unit_rows) : u.ntok * a.G;
+  u.ta0 = sp.s.first + tile * a.tpt;
+  const int ta1 = u.ta0 + u.ntok - 1;  // rows of the first and last token
+  u.L = sp.s.L;
+  u.lo = a.win >= u.ta0 ? 0 : u.ta0 - a.win;
+  u.hi = min(ta1 + 1, u.L);
+  u.start = u.lo & ~15;
+  const long long iu = (long long)u.t0 * a.c.Hkv + u.h;
+  u.idx = a.topk ? a.idx + iu * a.topk : nullptr;
+  u.slots = a.topk;
+  if (a.topk && a.topk_len) u.slots = min(u.slots, max(0, __ldg(a.topk_len + iu)));
+  u.table = a.c.table + cur.b * a.c.tstride;
+  cur.w0 += u.c1 - u.c0;
+  k8_next(cur);
+  return u;
 }
 
 template <int DK, int DV, bool ROWS, int FMT>
@@ -347,6 +391,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023);
   __shared__ int dead_word;
   __shared__ float q_scale[16];
+  __shared__ float meet[kK8Warps][32];  // maxima and sums of a unit's rows
   const K8Cache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gr = lane >> 2, q4 = lane & 3;
   if (tid == 0) dead_word = 0;
@@ -360,173 +405,202 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
     }
   }
   pdl_trigger();  // the join waits for this kernel's end, but need not be launched after it
+  pdl_wait();
 
   __shared__ K8Found found;
   K8Cursor cur;
   if (!k8_begin<128>(a, ws, tid, found, cur)) return;
-  float* const parts = k8_part(ws, gridDim.x, 2 * blockIdx.x, 16, DV);
+  float* part_out = k8_part(ws, gridDim.x, 2 * blockIdx.x, 16, DV);  // slot 0: the part that the share begins with
 
   uint8_t* const wsm = smem + warp * S * P::kData;
   uint32_t* const sq = reinterpret_cast<uint32_t*>(smem + P::kQAt);
   uint8_t* const wmeta = smem + P::kMetaAt + warp * S * P::kMeta;
+  const K8Unit* const units = reinterpret_cast<const K8Unit*>(smem + P::kUnitAt) + warp * P::kRing;
   const uint32_t sbase = smem_u32(wsm), mbase = smem_u32(wmeta), bar0 = smem_u32(bars);
   uint32_t phases = 0;  // of this warp's barriers
   int dead = 0;         // a wait gave up: no more copies, and NaN for a result
   const int krs = c.Hkv * DK, vrs = c.Hkv * DV;  // bytes from row to row of the cache
 
-  for (long long w = cur.w0; w < cur.w1;) {
-    k8_settle(a, cur);
-    const K8Span& sp = cur.sp;
-    const int b = cur.b, h = cur.h, ut = cur.ut, c0 = cur.c0, c1 = (int)min((long long)sp.ch, c0 + (cur.w1 - w));
-    // a KV head's units lie together, a token's parts of the heads innermost
-    const int tile = a.hs == 1 ? ut : ut / a.hs, hp = ut - tile * a.hs;
-    const int t0 = sp.s.t0 + tile * a.tpt, ntok = min(a.tpt, sp.s.n - tile * a.tpt);
-    const int head0 = h * a.G + hp * 16, rows = a.hs > 1 ? min(16, a.G - hp * 16) : ntok * a.G;
-    const int ta0 = sp.s.first + tile * a.tpt, ta1 = ta0 + ntok - 1;  // rows of the first and last token
-    const int lo_all = a.win >= ta0 ? 0 : ta0 - a.win, hi_all = min(ta1 + 1, sp.s.L);
-    const int lo_last = a.win >= ta1 ? 0 : ta1 - a.win;
-    const int start = lo_all & ~15;
-    const long long iu = (long long)t0 * c.Hkv + h;
-    const int* idx = a.topk ? a.idx + iu * a.topk : nullptr;
-    int slots = a.topk;
-    if (a.topk && a.topk_len) slots = min(slots, max(0, __ldg(a.topk_len + iu)));
-    const int* table = c.table + b * c.tstride;
-
-    // --- Q: warp w brings rows 4 w .. 4 w + 3, 8 lanes a row; the loads here, the rest behind the first copies
-    constexpr int kQw = DK / 64;  // 16-byte pieces of a lane: piece qp + 8 i of the row
-    const int qrow = warp * 4 + (lane >> 3), qp = lane & 7;
-    uint4 raw[kQw];
-    {
-      const int tok = k8_quot(a.by_gdiv, qrow);
-      const char* src = static_cast<const char*>(a.q) +
-                        ((long long)(t0 + tok) * a.qstride + (long long)(head0 + qrow - tok * a.gdiv) * DK) * 2;
-#pragma unroll
-      for (int i = 0; i < kQw; ++i)
-        raw[i] = qrow < rows ? __ldg(reinterpret_cast<const uint4*>(src + (qp + 8 * i) * 16)) : make_uint4(0, 0, 0, 0);
+  // --- The warp's fetching runs ahead of its computing, over the units of the share: a step's
+  // index is asked for two steps before its rows, and its page one.  Lane x of 32 (ROWS) or
+  // of 2 resolves row (or half) x of a step. ---
+  const int lane_row = warp * 32 + (ROWS ? lane : (lane & 1) * 16);
+  int fu = P::kRing - 1, fk = 0, fn = 0;  // the fetch's unit (ring slot), step of it, steps of it
+  auto advance = [&]() {                  // to the next step; fn = 0: none is left
+    if (++fk < fn) return;
+    fk = fn = 0;
+    if (cur.w0 >= cur.w1) return;
+    fu = (fu + 1) & (P::kRing - 1);
+    const K8Unit u = k8_take(a, cur);
+    if (lane == 0) const_cast<K8Unit*>(units)[fu] = u;
+    fn = u.c1 - u.c0;
+    __syncwarp();
+  };
+  auto fetch_idx = [&](int un, int k) -> int {  // of step k of unit un; un < 0: no step
+    if (!a.topk || un < 0) return 0;
+    const K8Unit& u = units[un];
+    const int slot = k8_quot(a.by_bs, (u.c0 + k) * kK8Chunk + lane_row);
+    return slot < u.slots ? __ldg(u.idx + slot) : -1;
+  };
+  auto resolve = [&](int un, int k, int x) -> int {  // its (first) row, -1: none
+    if (un < 0) return -1;
+    const K8Unit& u = units[un];
+    const int p = (u.c0 + k) * kK8Chunk + lane_row;
+    int row = u.start + p;
+    if (a.topk) {
+      if (x < 0) return -1;
+      if ((long long)x * a.bs >= u.L) {
+        if (c.status) atomicOr(c.status, kStatusIndexRange);
+        return -1;
+      }
+      row = x * a.bs + k8_rem(a.by_bs, p);
     }
+    const int last = ROWS ? row : row + 15;
+    return row < u.hi && last >= u.lo ? row : -1;
+  };
+  auto fetch_page = [&](int un, int row) -> int { return row >= 0 ? __ldg(units[un].table + k8_quot(c.by_ps, row)) : 0; };
+  int fx = 0, f_row = -1, f_page = 0, f_head = 0;
+  // the page of the step that the fetch stands at, then the index of the one behind it
+  auto look = [&]() {
+    const int un = fn ? fu : -1;
+    f_row = resolve(un, fk, fx);
+    f_page = fetch_page(un, f_row);
+    if (fn) f_head = units[fu].h;
+    advance();
+    fx = fetch_idx(fn ? fu : -1, fk);
+  };
+  auto issue = [&](int st, int row, int page, int head) {  // into stage st
+    if (row >= 0 && (page < 0 || page >= c.n_pages)) {
+      if (c.status) atomicOr(c.status, kStatusIndexRange);
+      row = -1;
+    }
+    const uint32_t dst = sbase + st * P::kData, meta = mbase + st * P::kMeta;
+    int* im = reinterpret_cast<int*>(wmeta + st * P::kMeta);
+    const int rr = row >= 0 ? page * c.ps + k8_rem(c.by_ps, row) : -1;  // row of the cache
+    const long long sc = (long long)page * c.Hkv + head;
+    if (ROWS) {
+      im[lane] = row;
+      if (row >= 0) {
+        k8_cp4(meta + 128 + 4 * lane, c.ks + sc);
+        k8_cp4(meta + 256 + 4 * lane, c.vs + sc);
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        k8_copy_rows<DK>(dst + x * 16 * DK, c.k + head * DK, krs, rr, 16 * x, lane);
+        k8_copy_rows<DV>(dst + 32 * DK + x * 16 * DV, c.v + head * DV, vrs, rr, 16 * x, lane);
+      }
+    } else {
+      const int both = (row >= 0) + __shfl_xor_sync(~0u, row >= 0, 1);
+      if (lane == 0 && both) mbar_arrive_tx(bars + st, both * 16 * (DK + DV));
+      __syncwarp();
+      if (lane < 2) {
+        im[lane] = row;
+        if (row >= 0) {
+          k8_cp4(meta + 8 + 4 * lane, c.ks + sc);
+          k8_cp4(meta + 16 + 4 * lane, c.vs + sc);
+          const uint32_t bar = bar0 + st * 8, kd = dst + lane * 16 * DK;
+          k8_box(kd, &maps.k, head, rr, bar);
+          if (DK == 192) k8_box(kd + 2048, &maps.k2, head, rr, bar);
+          k8_box(dst + 32 * DK + lane * 16 * DV, &maps.v, head, rr, bar);
+        }
+      }
+    }
+  };
+
+  // --- Q of a unit: warp w brings rows 4 w .. 4 w + 3, 8 lanes a row ---
+  constexpr int kQw = DK / 64;  // 16-byte pieces of a lane: piece qp + 8 i of the row
+  const int qrow = warp * 4 + (lane >> 3), qp = lane & 7;
+  uint4 raw[kQw];
+  auto load_q = [&](const K8Unit& u) {
+    const int tok = k8_quot(a.by_gdiv, qrow);
+    const char* src = static_cast<const char*>(a.q) +
+                      ((long long)(u.t0 + tok) * a.qstride + (long long)(u.head0 + qrow - tok * a.gdiv) * DK) * 2;
+#pragma unroll
+    for (int i = 0; i < kQw; ++i)
+      raw[i] = qrow < u.rows ? __ldg(reinterpret_cast<const uint4*>(src + (qp + 8 * i) * 16)) : make_uint4(0, 0, 0, 0);
+  };
+  auto lay_q = [&]() {
+    // halves times 2^(14 - E), E the exponent of the row's largest, in the MMA's order
+    float big = 0.f;
+#pragma unroll
+    for (int i = 0; i < kQw; ++i) {
+      const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = k8_two(v[j], a.f16);
+        big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+    }
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
+    const int E = big > 0.f ? max((int)(__float_as_uint(big) >> 23) - 127, -110) : 14;
+    const float mul = __uint_as_float((uint32_t)(14 - E + 127) << 23);
+    if (qp == 0) q_scale[qrow] = a.scale_log2 * __uint_as_float((uint32_t)(E - 14 + 127) << 23);
+#pragma unroll
+    for (int i = 0; i < kQw; ++i) {
+      // columns 64 i + 8 qp .. + 7, that is 16 q4' + 8 x with q4' = qp / 2, x = qp % 2
+      const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      uint32_t hh[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = k8_two(v[j], a.f16);
+        hh[j] = k8_halves(f.x * mul, f.y * mul);
+      }
+      // the lane that holds row qrow % 8 and columns q4' of the MMA; register r (+ 2 for the upper k);
+      // 4 columns are k 2 q4' + {0, 1 | 8, 9} of k step 4 i + 2 x + {0, 1}
+      const int to = (qrow & 7) * 4 + (qp >> 1), r = qrow >> 3;
+      uint32_t* dst = sq + ((4 * i + 2 * (qp & 1)) * 32 + to) * 4 + r;
+      dst[0] = hh[0];
+      dst[2] = hh[1];
+      dst[128] = hh[2];
+      dst[130] = hh[3];
+    }
+  };
+
+  {
+    // the first S steps, their indices and then their pages asked for together
+    int us[S + 2], ks[S + 2], xs[S + 2], rw[S + 1], pg[S + 1], hd[S + 1];
+#pragma unroll
+    for (int k = 0; k < S + 2; ++k) {
+      advance();
+      us[k] = fn ? fu : -1;
+      ks[k] = fk;
+      xs[k] = fetch_idx(us[k], fk);
+      if (k == 0) load_q(units[fu]);
+    }
+#pragma unroll
+    for (int k = 0; k < S + 1; ++k) {
+      rw[k] = resolve(us[k], ks[k], xs[k]);
+      pg[k] = fetch_page(us[k], rw[k]);
+      hd[k] = us[k] >= 0 ? units[us[k]].h : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      issue(k, rw[k], pg[k], hd[k]);
+      cp_async_commit();
+    }
+    f_row = rw[S];
+    f_page = pg[S];
+    f_head = hd[S];
+    fx = xs[S + 1];
+  }
+  lay_q();
+  __syncthreads();
+
+  long long left = cur.share.at(blockIdx.x + 1) - cur.share.at(blockIdx.x);  // chunks of the share
+  int at = 0;
+  for (int un = 0; left > 0; un = (un + 1) & (P::kRing - 1)) {
+    const K8Unit& u = units[un];
+    const int n_steps = u.c1 - u.c0, ta0 = u.ta0;
+    left -= n_steps;
+    const int lo_last = max(0, ta0 + u.ntok - 1 - a.win);
     int ta[2], lo[2];  // of this thread's rows gr and gr + 8
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      ta[r] = ta0 + min(k8_quot(a.by_gdiv, gr + 8 * r), ntok - 1);
-      lo[r] = a.win >= ta[r] ? 0 : ta[r] - a.win;
+      ta[r] = ta0 + min(k8_quot(a.by_gdiv, gr + 8 * r), u.ntok - 1);
+      lo[r] = max(0, ta[r] - a.win);
     }
-    const float sink = (tid >> 3) < rows ? k8_sink(a, head0 + k8_rem(a.by_gdiv, tid >> 3)) : -INFINITY;
-
-    // --- the steps of this warp: 32 rows of each chunk; lane x of 32 (ROWS) or of 2 resolves row (or half) x
-    const int n_steps = c1 - c0;
-    const int p0 = c0 * kK8Chunk + warp * 32 + (ROWS ? lane : (lane & 1) * 16);
-    auto fetch_idx = [&](int k) -> int {
-      if (!a.topk) return 0;
-      const int slot = k8_quot(a.by_bs, p0 + k * kK8Chunk);
-      return k < n_steps && slot < slots ? __ldg(idx + slot) : -1;
-    };
-    auto resolve = [&](int k, int x) -> int {  // the (first) row of step k, -1: none
-      if (k >= n_steps) return -1;
-      const int p = p0 + k * kK8Chunk;
-      int row = start + p;
-      if (a.topk) {
-        if (x < 0) return -1;
-        if ((long long)x * a.bs >= sp.s.L) {
-          if (c.status) atomicOr(c.status, kStatusIndexRange);
-          return -1;
-        }
-        row = x * a.bs + k8_rem(a.by_bs, p);
-      }
-      const int last = ROWS ? row : row + 15;
-      return row < hi_all && last >= lo_all ? row : -1;
-    };
-    auto fetch_page = [&](int row) -> int { return row >= 0 ? __ldg(table + k8_quot(c.by_ps, row)) : 0; };
-    auto issue = [&](int st, int row, int page) {
-      if (row >= 0 && (page < 0 || page >= c.n_pages)) {
-        if (c.status) atomicOr(c.status, kStatusIndexRange);
-        row = -1;
-      }
-      const uint32_t dst = sbase + st * P::kData, meta = mbase + st * P::kMeta;
-      int* im = reinterpret_cast<int*>(wmeta + st * P::kMeta);
-      const int rr = row >= 0 ? page * c.ps + k8_rem(c.by_ps, row) : -1;  // row of the cache
-      const long long sc = (long long)page * c.Hkv + h;
-      if (ROWS) {
-        im[lane] = row;
-        if (row >= 0) {
-          k8_cp4(meta + 128 + 4 * lane, c.ks + sc);
-          k8_cp4(meta + 256 + 4 * lane, c.vs + sc);
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          k8_copy_rows<DK>(dst + x * 16 * DK, c.k + h * DK, krs, rr, 16 * x, lane);
-          k8_copy_rows<DV>(dst + 32 * DK + x * 16 * DV, c.v + h * DV, vrs, rr, 16 * x, lane);
-        }
-      } else {
-        const int both = (row >= 0) + __shfl_xor_sync(~0u, row >= 0, 1);
-        if (lane == 0 && both) mbar_arrive_tx(bars + st, both * 16 * (DK + DV));
-        __syncwarp();
-        if (lane < 2) {
-          im[lane] = row;
-          if (row >= 0) {
-            k8_cp4(meta + 8 + 4 * lane, c.ks + sc);
-            k8_cp4(meta + 16 + 4 * lane, c.vs + sc);
-            const uint32_t bar = bar0 + st * 8, kd = dst + lane * 16 * DK;
-            k8_box(kd, &maps.k, h, rr, bar);
-            if (DK == 192) k8_box(kd + 2048, &maps.k2, h, rr, bar);
-            k8_box(dst + 32 * DK + lane * 16 * DV, &maps.v, h, rr, bar);
-          }
-        }
-      }
-    };
-
-    int xs[S + 1], rw[S], pg[S];
-#pragma unroll
-    for (int k = 0; k <= S; ++k) xs[k] = fetch_idx(k);
-#pragma unroll
-    for (int k = 0; k < S; ++k) {
-      rw[k] = resolve(k, xs[k]);
-      pg[k] = fetch_page(rw[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < S; ++k) {
-      if (!dead) issue(k, rw[k], pg[k]);
-      cp_async_commit();
-    }
-    int next_x = fetch_idx(S + 1), next_row = resolve(S, xs[S]), next_page = fetch_page(next_row);
-
-    // Q as halves times 2^(14 - E), E the exponent of the row's largest, in the MMA's order
-    {
-      float big = 0.f;
-#pragma unroll
-      for (int i = 0; i < kQw; ++i) {
-        const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = k8_two(v[j], a.f16);
-          big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-      }
-#pragma unroll
-      for (int d = 1; d < 8; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
-      const int E = big > 0.f ? max((int)(__float_as_uint(big) >> 23) - 127, -110) : 14;
-      const float mul = __uint_as_float((uint32_t)(14 - E + 127) << 23);
-      if (qp == 0) q_scale[qrow] = a.scale_log2 * __uint_as_float((uint32_t)(E - 14 + 127) << 23);
-#pragma unroll
-      for (int i = 0; i < kQw; ++i) {
-        // columns 64 i + 8 qp .. + 7, that is 16 q4' + 8 x with q4' = qp / 2, x = qp % 2
-        const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        uint32_t hh[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = k8_two(v[j], a.f16);
-          hh[j] = k8_halves(f.x * mul, f.y * mul);
-        }
-        // the lane that holds row qrow % 8 and columns q4' of the MMA; register r (+ 2 for the upper k)
-        const int to = (qrow & 7) * 4 + (qp >> 1), r = qrow >> 3;
-        // 4 columns are k 2 q4' + {0, 1 | 8, 9} of k step 4 i + 2 x + {0, 1}
-        uint32_t* dst = sq + ((4 * i + 2 * (qp & 1)) * 32 + to) * 4 + r;
-        dst[0] = hh[0];
-        dst[2] = hh[1];
-        dst[128] = hh[2];
-        dst[130] = hh[3];
-      }
-    }
-    __syncthreads();
+    const float sink = (tid >> 3) < u.rows ? k8_sink(a, u.head0 + k8_rem(a.by_gdiv, tid >> 3)) : -INFINITY;
     const float fr[2] = {q_scale[gr], q_scale[gr + 8]};
 
     float o[DV / 16][2][4];
@@ -539,7 +613,6 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float base[2] = {0.f, 0.f}, limit[2] = {-INFINITY, -INFINITY};  // m - kK8Top, and how far above it w may lie
 
-    int at = 0;
     for (int k = 0; k < n_steps; ++k) {
       k8_cp_wait<S - 1>();
       __syncwarp();
@@ -629,8 +702,14 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
         if (FMT == kFmtE4M3 && !full) {
           // A NaN in a V row that some of the unit's rows do not see (a stale row of the page,
           // a later token's): the product would carry it (0 * NaN) to all of them.  It is set
-          // into the rows that see it here, and out of the tile.  (A half without rows is
-          // whatever the stage held before.)
+          // into the rows that see it here, and out of the tile.  (A half without rows, which
+          // holds whatever the stage did before, becomes zeros.)
+          if (!ROWS && (row0[0] < 0 || row0[1] < 0)) {
+            for (int i = lane; i < DV; i += 32)
+              *reinterpret_cast<uint4*>(stv + (row0[0] < 0 ? 0 : 16 * DV) + i * 16) = make_uint4(0, 0, 0, 0);
+            fence_async_smem();
+            __syncwarp();
+          }
           uint32_t nan = 0;
 #pragma unroll
           for (int i = 0; i < DV / 16; ++i) {
@@ -737,89 +816,91 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
           }
         }
       }
-      __syncwarp();  // the stage has been read
-      if (!dead) issue(at, next_row, next_page);
+      if (k + 1 == n_steps) break;  // the last stage takes this warp's O first
+      __syncwarp();                 // the stage has been read
+      if (!dead) issue(at, f_row, f_page, f_head);
       cp_async_commit();
-      next_row = resolve(k + S + 1, next_x);
-      next_page = fetch_page(next_row);
-      next_x = fetch_idx(k + S + 2);
+      look();
       at = at + 1 == S ? 0 : at + 1;
     }
-    k8_cp_wait<0>();
-    if (dead) {
-      if (!ROWS)
-        for (int i = 0; i < S; ++i) mbar_wait_drain(bars + i, (phases >> i) & 1);
-      l[0] = l[1] = __int_as_float(0x7fffffff);
-    }
-    __syncwarp();
+    if (dead) l[0] = l[1] = __int_as_float(0x7fffffff);
 
-    // --- the warps' results meet: maximum, sum, O --------------------------------
-    float* fo = reinterpret_cast<float*>(wsm);
-    float* fm = fo + 16 * P::kLd;
+    // --- the warps' results meet: maximum, sum, O (rows of DV floats, odd rows' 64-byte halves swapped) ---
+    float* const fo = reinterpret_cast<float*>(wsm + at * P::kData);
+    __syncwarp();
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(~0u, l[r], 1);
       l[r] += __shfl_xor_sync(~0u, l[r], 2);
+      const int row = gr + 8 * r;
       if (q4 == 0) {
-        fm[gr + 8 * r] = m[r];
-        fm[16 + gr + 8 * r] = l[r];
+        meet[warp][row] = m[r];
+        meet[warp][16 + row] = l[r];
       }
 #pragma unroll
       for (int i = 0; i < DV / 16; ++i)
-        *reinterpret_cast<float4*>(fo + (gr + 8 * r) * P::kLd + 16 * i + 4 * q4) =
+        *reinterpret_cast<float4*>(fo + row * DV + 4 * ((4 * i + q4) ^ ((row & 1) << 2))) =
             make_float4(o[i][0][2 * r], o[i][1][2 * r], o[i][0][2 * r + 1], o[i][1][2 * r + 1]);
     }
+    if (left > 0) load_q(units[(un + 1) & (P::kRing - 1)]);
     __syncthreads();
     {
       const int row = tid >> 3, part = tid & 7;
-      const float* f0 = reinterpret_cast<const float*>(smem);
+      // all warps have taken the same number of steps: the same stage holds their O
+      const float* f0 = reinterpret_cast<const float*>(smem + at * P::kData);
       constexpr int kW = S * P::kData / 4;
       float mw[kK8Warps], top = -INFINITY, total = 0.f;
 #pragma unroll
       for (int x = 0; x < kK8Warps; ++x) {
-        mw[x] = f0[x * kW + 16 * P::kLd + row];
+        mw[x] = meet[x][row];
         top = fmaxf(top, mw[x]);
       }
 #pragma unroll
       for (int x = 0; x < kK8Warps; ++x) {
         mw[x] = top == -INFINITY ? 1.f : ex2_approx(mw[x] - top);
-        total = fmaf(f0[x * kW + 16 * P::kLd + 16 + row], mw[x], total);
+        total = fmaf(meet[x][16 + row], mw[x], total);
       }
-      const bool whole = c0 == 0 && c1 == sp.ch;
-      // a part of a unit: slot 0 holds the one that this CTA's share begins with
-      float* part_out = parts + (w == cur.w0 ? 0 : k8_part_floats(16, DV));
-      if (row < rows) {
-        const int tok = k8_quot(a.by_gdiv, row), t = t0 + tok, head = head0 + row - tok * a.gdiv;
+      const bool whole = u.c0 == 0 && u.c1 == u.ch;
+      if (row < u.rows) {
+        const int tok = k8_quot(a.by_gdiv, row), t = u.t0 + tok, head = u.head0 + row - tok * a.gdiv;
         float lse, norm = 0.f;
         if (whole) norm = k8_norm(sink, top, total, &lse);
         if (whole && part == 0) a.lse[(long long)t * a.Hq + head] = lse;
 #pragma unroll
         for (int i = 0; i < DV / 32; ++i) {
-          const int d = 4 * (part + 8 * i);
+          const int col = part + 8 * i;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int x = 0; x < kK8Warps; ++x) {
-            const float4 y = *reinterpret_cast<const float4*>(f0 + x * kW + row * P::kLd + d);
+            const float4 y = *reinterpret_cast<const float4*>(f0 + x * kW + row * DV + 4 * (col ^ ((row & 1) << 2)));
             v.x = fmaf(y.x, mw[x], v.x);
             v.y = fmaf(y.y, mw[x], v.y);
             v.z = fmaf(y.z, mw[x], v.z);
             v.w = fmaf(y.w, mw[x], v.w);
           }
-          if (whole) k8_store(a, t, head, d, norm, v);
-          else *reinterpret_cast<float4*>(part_out + 32 + row * DV + d) = v;
+          if (whole) k8_store(a, t, head, 4 * col, norm, v);
+          else *reinterpret_cast<float4*>(part_out + 32 + row * DV + 4 * col) = v;
         }
         if (!whole && part == 0) {
           part_out[row] = top;
           part_out[16 + row] = total;
         }
       }
-      if (!whole && tid == 0) k8_note(ws, cur, t0, head0, rows, a.gdiv);
+      if (!whole && tid == 0) k8_note(ws, cur.share, u.begin, u.c0, u.ch, u.t0, u.head0, u.rows, a.gdiv);
     }
-    fence_async_smem();  // the copies that fill the stages again come behind these accesses
+    // slot 1: any later part
+    part_out = k8_part(ws, gridDim.x, 2 * blockIdx.x + 1, 16, DV);
+    if (left > 0) lay_q();  // every warp has taken the scores of this unit
+    fence_async_smem();     // the copies that fill the stage again come behind these accesses
     __syncthreads();
-    w += c1 - c0;
-    k8_next(cur);
+    if (!dead) issue(at, f_row, f_page, f_head);
+    cp_async_commit();
+    look();
+    at = at + 1 == S ? 0 : at + 1;
   }
+  k8_cp_wait<0>();
+  if (dead && !ROWS)
+    for (int i = 0; i < S; ++i) mbar_wait_drain(bars + i, (phases >> i) & 1);
 }
 
 // The units that span several CTAs.  The n blocks that held a part of a unit share its
@@ -932,9 +1013,8 @@ static cudaError_t split_t(const K8Fwd& a, void* ws, cudaStream_t st) {
       return cudaErrorInvalidValue;
   }
   const int n = k8_ctas(a);
-  k<<<(unsigned)n, 128, P::kSmem, st>>>(a, maps, static_cast<float*>(ws));
   count_launch();
-  e = cudaGetLastError();
+  e = launch_pdl(k, (unsigned)n, 128, P::kSmem, st, a, maps, static_cast<float*>(ws));
   if (e != cudaSuccess || n == 1) return e;
   count_launch();
   return launch_pdl(k8_join_kernel<16, DV>, (unsigned)n, 256, 0, st, a, static_cast<float*>(ws), n);
@@ -1345,7 +1425,8 @@ __global__ void __launch_bounds__(256, 1) k8_latent_kernel(const __grid_constant
           else *reinterpret_cast<float4*>(part_out + 2 * R + row * kLatDV + d) = v;
         }
       }
-    if (!whole && tid == 0) k8_note(ws, cur, t, head0, rows, a.gdiv);
+    if (!whole && tid == 0)
+      k8_note(ws, cur.share, cur.seq_at + ((long long)cur.h * sp.per_h + cur.ut) * sp.ch, c0, sp.ch, t, head0, rows, a.gdiv);
     __syncthreads();  // red, q_scale, the stages and Q are written again
     w += c1 - c0;
     k8_next(cur);
