@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -108,6 +109,16 @@ int64_t token_step(const at::Tensor& t, const char* name, int64_t heads, int64_t
   return step;
 }
 
+// n elements of `type` in the memory of `all`, from element `from` on (a view would cost as much as an
+// allocation).
+at::Tensor part_of(const at::Tensor& all, at::ScalarType type, int64_t from, int64_t n) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                          c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_storage_offset(from);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  return t;
+}
+
 int32_t to_i32(int64_t v, const char* name) {
   if (v < INT32_MIN || v > INT32_MAX) value_error(std::string(name) + " does not fit 32 bits");
   return (int32_t)v;
@@ -189,9 +200,12 @@ PyObject* kv8_plan(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
   a.page_size = to_i32(integer(v[5], "page_size"), "page_size");
   a.n_tokens = to_i32(integer(v[6], "n_tokens"), "n_tokens");
   void* st = stream_of(v[7], index);
-  const at::TensorOptions i32 = old.options();
-  at::Tensor lens = at::empty({B}, i32), cu = at::empty({B + 1}, i32), left = at::empty({1}, i32),
-             served = at::empty({1}, i32), slots = at::empty({a.n_tokens > 0 ? a.n_tokens : 0}, i32.dtype(at::kLong));
+  // one allocation: slots, then the int32 outputs
+  const int64_t T = a.n_tokens > 0 ? a.n_tokens : 0;
+  const at::Tensor all = at::empty({T + B + 2}, old.options().dtype(at::kLong));
+  const at::Tensor slots = part_of(all, at::kLong, 0, T), lens = part_of(all, at::kInt, 2 * T, B),
+                   cu = part_of(all, at::kInt, 2 * T + B, B + 1), left = part_of(all, at::kInt, 2 * T + 2 * B + 1, 1),
+                   served = part_of(all, at::kInt, 2 * T + 2 * B + 2, 1);
   a.seq_lens = static_cast<int32_t*>(lens.data_ptr());
   a.cu_seqlens_q = static_cast<int32_t*>(cu.data_ptr());
   a.n_free_out = static_cast<int32_t*>(left.data_ptr());
@@ -290,9 +304,9 @@ PyObject* kv8_attend(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
   size_t bytes = 0;
   sa_status status = sa_kv8_fwd_get_workspace_size(&c, &a, &bytes);
   if (status != SA_OK) return PyLong_FromLong(status);
-  const at::Tensor ws = at::empty({(int64_t)bytes}, q.options().dtype(at::kByte));
   const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
-  status = sa_kv8_fwd(&c, &a, ws.data_ptr(), bytes, st);
+  const c10::DataPtr ws = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
+  status = sa_kv8_fwd(&c, &a, ws.get(), bytes, st);
   if (status != SA_OK) return PyLong_FromLong(status);
   PyObject* r = PyTuple_New(2);
   if (!r) return nullptr;
