@@ -277,13 +277,76 @@ __device__ __forceinline__ int k8_find_warp(const K8Cache& c, int t, int lane) {
   return lo;
 }
 
-// One CTA per (window of tokens, head): it takes the page runs that begin in its
-// window (a run is the new rows of one page; a page's runs never split over CTAs, so
-// scale and codes have one writer).  NT threads write K and as many V.  Bound by the
-// bytes for prompts (2 in, 1 out per element), by the chain offsets -> length -> table ->
-// scale for a row per request.
+// A run is the new rows of one page; it has one writer, so the scale and the codes do too.
+//
+// Where requests bring many rows, a CTA takes a run, a head, and K or V: the first threads
+// of the grid's x range find run x over the requests' page counts.  Bound by the bytes (2
+// in, 1 out per element) and, a run at a time, by the chain offsets -> rows -> maximum ->
+// codes; CTAs enough that an SM holds several.
+template <bool F16, int NT>
+__global__ void __launch_bounds__(NT, NT == 512 ? 1 : 6) kv8_write_runs_kernel(const __grid_constant__ K8Write a) {
+  __shared__ float red[NT / 32];
+  __shared__ int sums[NT / 32];
+  __shared__ int found[4];  // first token, rows, page of the sequence, offset
+  __shared__ const int* found_table;
+  const K8Cache& c = a.c;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y, half = blockIdx.z;
+  const int per = (c.B + NT - 1) / NT, b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
+  K8Seq s = {};
+  auto pages = [&](const K8Seq& q) {  // pages that get rows
+    const int first = max(q.first, 0);
+    return q.n > 0 && q.L > first ? k8_quot(c.by_ps, q.L - 1) - k8_quot(c.by_ps, first) + 1 : 0;
+  };
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    s = k8_seq(c, b);
+    mine += pages(s);
+  }
+  int inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(~0u, inc, d);
+    if (lane >= d) inc += x;
+  }
+  if (lane == 31) sums[warp] = inc;
+  __syncthreads();
+  int at = inc - mine, total = 0;
+#pragma unroll
+  for (int x = 0; x < NT / 32; ++x) {
+    if (x < warp) at += sums[x];
+    total += sums[x];
+  }
+  const int run = blockIdx.x;
+  if (run >= total) return;
+  if (at <= run && run < at + mine) {
+    for (int b = b0;; ++b) {
+      if (b1 - b0 > 1) s = k8_seq(c, b);
+      const int n = pages(s);
+      if (run < at + n) {
+        const int first = max(s.first, 0), j = k8_quot(c.by_ps, first) + run - at, pos = max(first, j * c.ps);
+        found[0] = s.t0 + pos - s.first;
+        found[1] = min((j + 1) * c.ps, s.L) - pos;
+        found[2] = j;
+        found[3] = pos - j * c.ps;
+        found_table = c.table + b * c.tstride + j;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  const int t = found[0], d = half ? c.dv : c.dqk;
+  const char* x = half ? static_cast<const char*>(a.v) + (t * a.vstride + (long long)h * d) * 2
+                       : static_cast<const char*>(a.k) + (t * a.kstride + (long long)h * d) * 2;
+  k8_write_part<F16, NT>(x, half ? a.vstride : a.kstride, found[1], d, half ? a.by_v : a.by_k, c, found_table,
+                         half ? c.v : c.k, half ? c.vs : c.ks, h, found[3], tid, 1, red);
+}
+
+// Where they bring a few rows each, a CTA takes the runs that begin in its window of
+// tokens (one token, unless there are many), NT threads for K and as many for V.  Bound by
+// the chain offsets -> length -> table -> scale.
 template <bool F16, int NT, bool SHARED>
-__global__ void __launch_bounds__(SHARED ? NT : 2 * NT, NT == 512 ? 1 : NT == 128 ? 3 : 8) kv8_write_kernel(const __grid_constant__ K8Write a) {
+__global__ void __launch_bounds__(SHARED ? NT : 2 * NT, 8) kv8_write_kernel(const __grid_constant__ K8Write a) {
   __shared__ float red[2][NT / 32];
   const K8Cache& c = a.c;
   const int h = blockIdx.y, half = SHARED ? 0 : threadIdx.x / NT, tid = SHARED ? threadIdx.x : threadIdx.x % NT;
@@ -318,30 +381,32 @@ __global__ void __launch_bounds__(SHARED ? NT : 2 * NT, NT == 512 ? 1 : NT == 12
   }
 }
 
-template <int NT, bool SHARED>
-static void write_t(const K8Write& a, dim3 grid, cudaStream_t st) {
-  const unsigned block = SHARED ? NT : 2 * NT;
-  if (a.f16) kv8_write_kernel<true, NT, SHARED><<<grid, block, 0, st>>>(a);
-  else kv8_write_kernel<false, NT, SHARED><<<grid, block, 0, st>>>(a);
-}
-
 cudaError_t launch_kv8_write(K8Write a, cudaStream_t st) {
-  if (a.c.T == 0 || a.c.B == 0) return cudaSuccess;
-  // threads for a page's rows where the requests bring many, for a few rows otherwise; about
-  // as many CTAs as the SMs hold then, each with a run or so (a CTA per 18 tokens, most of
-  // which found no run, took 31 us where this takes 17: 10 k tokens, 4 heads of 192 / 128)
-  const bool many = a.c.T >= 8ll * a.c.B;
-  const long long items = (long long)a.c.T * a.c.Hkv;
-  a.window = (int)max(1ll, items / (148 * (many ? 4 : 16)));
-  const dim3 grid((unsigned)((a.c.T + a.window - 1) / a.window), (unsigned)a.c.Hkv);
-  a.by_k = k8_div_of(a.c.dqk / 8);
-  a.by_v = k8_div_of(a.c.dv / 8);
-  if (a.c.shared) {
-    if (many) write_t<512, true>(a, grid, st);
-    else write_t<64, true>(a, grid, st);
+  const K8Cache& c = a.c;
+  if (c.T == 0 || c.B == 0) return cudaSuccess;
+  a.by_k = k8_div_of(c.dqk / 8);
+  a.by_v = k8_div_of(c.dv / 8);
+  // 8 rows per request on average: 10 k tokens of 7 prompts, 4 heads of 192 / 128, took 31 us
+  // window by window
+  if (c.T >= 8ll * c.B) {
+    const dim3 grid((unsigned)(c.T / c.ps + 2 * c.B), (unsigned)c.Hkv, c.shared ? 1 : 2);
+    if (c.dqk > 192) {
+      if (a.f16) kv8_write_runs_kernel<true, 512><<<grid, 512, 0, st>>>(a);
+      else kv8_write_runs_kernel<false, 512><<<grid, 512, 0, st>>>(a);
+    } else {
+      if (a.f16) kv8_write_runs_kernel<true, 128><<<grid, 128, 0, st>>>(a);
+      else kv8_write_runs_kernel<false, 128><<<grid, 128, 0, st>>>(a);
+    }
   } else {
-    if (many) write_t<128, false>(a, grid, st);
-    else write_t<32, false>(a, grid, st);
+    a.window = (int)max(1ll, (long long)c.T * c.Hkv / (148 * 16));
+    const dim3 grid((unsigned)((c.T + a.window - 1) / a.window), (unsigned)c.Hkv);
+    if (c.shared) {
+      if (a.f16) kv8_write_kernel<true, 64, true><<<grid, 64, 0, st>>>(a);
+      else kv8_write_kernel<false, 64, true><<<grid, 64, 0, st>>>(a);
+    } else {
+      if (a.f16) kv8_write_kernel<true, 32, false><<<grid, 64, 0, st>>>(a);
+      else kv8_write_kernel<false, 32, false><<<grid, 64, 0, st>>>(a);
+    }
   }
   count_launch();
   return cudaGetLastError();
