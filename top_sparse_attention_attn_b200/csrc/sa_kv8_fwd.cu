@@ -37,11 +37,11 @@ bool k8_built(int dqk, int dv, bool shared) {
 // largest is lost).  V's scale goes into the exponent: with w_j = s_j + log2 vs_j the
 // products use p'_j = 2^(w_j - max w), and the sum gets p'_j / vs_j.  So P needs one
 // exponential, and its 11 bits sit where the products are largest whatever the pages'
-// scales are.  p' <= 2^15: the maximum is let grow by up to 2^4 before O is rescaled,
-// and is held at 2^11.
+// scales are.  p' <= 2^15: the maximum is held at 2^7 and let grow by up to 2^8 before O is
+// rescaled; halves reach 2^-31 of the held one.
 constexpr int kK8Warps = 4;
 constexpr int kK8Chunk = 32 * kK8Warps;
-constexpr float kK8Grow = 4.f, kK8Top = 11.f;
+constexpr float kK8Grow = 8.f, kK8Top = 7.f;
 
 // A unit, or a share's part of it, as its warps know it.
 struct alignas(16) K8Unit {
@@ -260,6 +260,7 @@ struct K8Found {
   K8Span sp;
 };
 // The line's length, this CTA's share and the unit that it begins in; false: it has none.
+// NT threads look at the sequences; threads behind them come along.
 template <int NT>
 __device__ __forceinline__ bool k8_begin(const K8Fwd& a, float* ws, int tid, K8Found& f, K8Cursor& cur) {
   const int lane = tid & 31, warp = tid >> 5, B = a.c.B;
@@ -276,7 +277,7 @@ __device__ __forceinline__ bool k8_begin(const K8Fwd& a, float* ws, int tid, K8F
     const long long x = __shfl_up_sync(~0u, inc, d);
     if (lane >= d) inc += x;
   }
-  if (lane == 31) f.sum[warp] = inc;
+  if (lane == 31 && warp < NT / 32) f.sum[warp] = inc;
   __syncthreads();
   long long W = 0, at = inc - mine;
 #pragma unroll
@@ -284,7 +285,11 @@ __device__ __forceinline__ bool k8_begin(const K8Fwd& a, float* ws, int tid, K8F
     W += f.sum[x];
     if (x < warp) at += f.sum[x];
   }
-  const int n_cta = (int)min(W, (long long)gridDim.x);  // a share is empty only in CTAs behind these
+  int n_cta = (int)min(W, (long long)gridDim.x);  // a share is empty only in CTAs behind these
+  // Units of one length, and nearly as many as CTAs: one each.  Cutting them evenly would
+  // leave parts to join (131 KB each of 64 heads x 512), which costs as much as 5 chunks.
+  if (a.whole_units && a.sel_ch && W <= (long long)gridDim.x * a.sel_ch && 5 * W >= 3ll * gridDim.x * a.sel_ch)
+    n_cta = (int)(W / a.sel_ch);
   if (tid < 2) (reinterpret_cast<K8Join*>(ws) + 2 * blockIdx.x)[tid].n = 0;
   if (blockIdx.x >= n_cta) return false;
   if (W <= 0x7fffffff) {
@@ -1433,6 +1438,431 @@ __global__ void __launch_bounds__(256, 1) k8_latent_kernel(const __grid_constant
   }
 }
 
+// ---------------------------------------------------------------------------
+// the same with more than 32 heads: tcgen05
+// ---------------------------------------------------------------------------
+// A unit is one token and 64 of its heads; 128 rows per chunk, one CTA per SM.  The rows
+// lie along the MMA's M:
+//   S^T [128 rows x 64 heads] = K [128 x 576] Q^T       (K and Q K-major)
+//   O^T [4 x 128 columns x 64 heads] += V^T P^T         (V the first 8 slabs of K, MN-major)
+// so that K is converted once and serves both products, O stays in TMEM (256 columns) and a
+// thread holds a row's scores.  Shared memory holds one chunk as halves (147 KB, 9 slabs of
+// 64 columns) and Q (74 KB); P^T takes the slab of the last 64 columns, which only the scores
+// need.  Eight warps fetch the next chunk's codes into registers, convert them slab by
+// slab as the MMAs of the chunk before let go of the slabs, and do the softmax; a ninth
+// issues (of a third warpgroup, which gives its registers to the other two).  Bound: the MMAs, 36 + 32 at N = 64 and 44.5 cycles each (3026 per chunk), and the
+// softmax between the two products, which nothing overlaps.
+constexpr int kTcRows = 128, kTcSlab = kTcRows * 128, kTcSlabs = 9;
+struct K8Tc {
+  static constexpr int kQAt = kTcSlabs * kTcSlab;
+  static constexpr int kMetaAt = kQAt + 9 * 64 * 128;       // [2][128] rows seen, [2][128] scales
+  static constexpr int kHeadAt = kMetaAt + 2 * kTcRows * 8;  // [64] (fr, base)
+  static constexpr int kRedAt = kHeadAt + 64 * 8;            // [4][64]
+  static constexpr int kBarAt = kRedAt + 4 * 64 * 4;         // full [9], p_full, s_done, free [4]
+  static constexpr int kSmem = kBarAt + 16 * 8 + 1024;
+  static constexpr uint32_t kTmemS = 256;  // column of S^T behind the four blocks of O^T
+};
+__host__ __device__ constexpr uint32_t k8_idesc(int M, int N, bool a_mn, bool b_mn) {  // halves, fp32 sums
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+// Of the eight converting warps: a barrier, and whether any thread says yes.
+__device__ __forceinline__ void tc_bar() { asm volatile("bar.sync 1, 256;\n" ::: "memory"); }
+__device__ __forceinline__ bool tc_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n barrier.cta.red.or.pred p, 1, 256, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K8Fwd a, float* ws) {
+  using P = K8Tc;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023);
+  __shared__ K8Found found;
+  __shared__ uint32_t tmem_at;
+  __shared__ int abort_word, fresh;  // fresh: the chunk begins a part, O^T is overwritten
+  const K8Cache& c = a.c;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + P::kBarAt);
+  uint64_t *const p_full = full + 9, *const s_done = full + 10, *const blk_free = full + 11;
+  if (tid == 0) {
+    for (int i = 0; i < 10; ++i) mbar_init(full + i, 8);
+    for (int i = 10; i < 15; ++i) mbar_init(full + i, 1);
+    mbar_fence_init();
+    abort_word = 0;
+  }
+  if (warp == 8) {
+    tmem_alloc(&tmem_at, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  pdl_trigger();
+  pdl_wait();
+  K8Cursor cur;
+  const bool some = k8_begin<256>(a, ws, tid, found, cur);
+  const long long n_chunks = some ? cur.w1 - cur.w0 : 0;
+
+  // 384 threads launch with 168 registers: 2 x 128 x 232 + 128 x 40 are as many
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
+    // --- the MMAs ---
+    if (warp == 8 && lane == 0 && some) {
+      const uint32_t kat = smem_u32(smem), qat = kat + P::kQAt, pat = kat + 8 * kTcSlab;
+      const uint64_t dk = sdesc(kat, 0, 1024), dq = sdesc(qat, 0, 1024);
+      const uint64_t dv = sdesc(kat, kTcSlab, 1024), dp = sdesc(pat, kTcSlab, 1024);
+      constexpr uint32_t id_s = k8_idesc(128, 64, false, false), id_o = k8_idesc(128, 64, true, true);
+      for (long long n = 0; n < n_chunks; ++n) {
+        const uint32_t ph = (uint32_t)(n & 1);
+        bool ok = true;
+#pragma unroll 1
+        for (int sl = 0; sl < kTcSlabs && ok; ++sl) {
+          ok = mbar_wait(full + sl, ph, &abort_word, c.status);
+          tc_fence_after();
+          if (!ok) break;
+          const uint64_t A = desc_add(dk, sl * kTcSlab), B = desc_add(dq, sl * 8192);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mma_bf16(tmem + P::kTmemS, desc_add(A, 32 * e), desc_add(B, 32 * e), id_s, sl || e);
+        }
+        if (!ok) break;
+        mma_commit(s_done);
+        if (!mbar_wait(p_full, ph, &abort_word, c.status)) break;
+        tc_fence_after();
+        const bool over = *(volatile int*)&fresh != 0;
+#pragma unroll 1
+        for (int mb = 0; mb < 4; ++mb) {
+          const uint64_t A = desc_add(dv, mb * 2 * kTcSlab);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mma_bf16(tmem + mb * 64, desc_add(A, 2048 * e), desc_add(dp, 2048 * e), id_o, !over || e);
+          mma_commit(blk_free + mb);
+        }
+      }
+      if (abort_word) mbar_wait_drain(blk_free + 3, 0);  // bounded: what was issued before the wait gave up
+    }
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
+    uint32_t* const see_of = reinterpret_cast<uint32_t*>(smem + P::kMetaAt);         // [2][128]
+    float* const scale_of = reinterpret_cast<float*>(smem + P::kMetaAt) + 2 * kTcRows;  // [2][128]
+    float2* const head_of = reinterpret_cast<float2*>(smem + P::kHeadAt);            // [64] fr, base
+    float* const red = reinterpret_cast<float*>(smem + P::kRedAt);                   // [4][64]
+    const uint32_t tm_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const int hh = warp >> 2, row_j = 32 * (warp & 3) + lane;  // this thread's heads and row in the softmax
+    const int krs = c.Hkv * kLatDK;
+    float* part_out = k8_part(ws, gridDim.x, 2 * blockIdx.x, 64, kLatDV);
+    bool dead = false;
+    long long n = 0;  // chunks done
+    while (n < n_chunks) {
+      const K8Unit u = k8_take(a, cur);
+      const int n_steps = u.c1 - u.c0;
+      // rows of a chunk: warp w looks up and converts rows 16 w .. 16 w + 15 (lane x: row x % 16)
+      const int p0 = u.c0 * kTcRows + warp * 16 + (lane & 15);
+      auto fetch_idx = [&](int k) -> int {
+        if (!a.topk) return 0;
+        const int slot = k8_quot(a.by_bs, p0 + k * kTcRows);
+        return k < n_steps && slot < u.slots ? __ldg(u.idx + slot) : -1;
+      };
+      auto resolve = [&](int k, int x) -> int {
+        if (k >= n_steps) return -1;
+        const int p = p0 + k * kTcRows;
+        int row = u.start + p;
+        if (a.topk) {
+          if (x < 0) return -1;
+          if ((long long)x * a.bs >= u.L) {
+            if (c.status) atomicOr(c.status, kStatusIndexRange);
+            return -1;
+          }
+          row = x * a.bs + k8_rem(a.by_bs, p);
+        }
+        return row < u.hi && row >= u.lo ? row : -1;
+      };
+      auto fetch_page = [&](int row) -> int { return row >= 0 ? __ldg(u.table + k8_quot(c.by_ps, row)) : 0; };
+      // the lane's two rows of the codes and its row's scale, from what was looked up
+      const uint8_t* ptr[2];
+      float ks_next = 0.f;
+      bool see_next = false;
+      auto point = [&](int row, int page) {
+        if (row >= 0 && (page < 0 || page >= c.n_pages)) {
+          if (c.status) atomicOr(c.status, kStatusIndexRange);
+          row = -1;
+        }
+        const int rr = row >= 0 ? page * c.ps + k8_rem(c.by_ps, row) : -1;
+        see_next = row >= 0;
+        if (see_next) ks_next = __ldg(c.ks + (long long)page * c.Hkv + u.h);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int at = __shfl_sync(~0u, rr, 8 * j + (lane >> 2));
+          ptr[j] = at >= 0 ? c.k + (long long)at * krs + u.h * kLatDK + (lane & 3) * 16 : nullptr;
+        }
+      };
+      int x0 = fetch_idx(0), x1 = fetch_idx(1), next_x = fetch_idx(2);
+      const int row0 = resolve(0, x0), pg0 = fetch_page(row0);
+      int next_row = resolve(1, x1), next_page = fetch_page(next_row);
+      uint4 raw[9][2];
+      point(row0, pg0);
+#pragma unroll
+      for (int sl = 0; sl < 9; ++sl)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          raw[sl][j] = ptr[j] ? __ldg(reinterpret_cast<const uint4*>(ptr[j] + sl * 64)) : make_uint4(0, 0, 0, 0);
+
+      // --- Q, 8 lanes a row, as halves times 2^(14 - E); the scores of the unit before have been taken ---
+      uint4 qr[2][9];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int row = 32 * y + warp * 4 + (lane >> 3);
+        const char* src = static_cast<const char*>(a.q) + ((long long)u.t0 * a.qstride + (long long)(u.head0 + row) * kLatDK) * 2;
+#pragma unroll
+        for (int i = 0; i < 9; ++i)
+          qr[y][i] = row < u.rows ? __ldg(reinterpret_cast<const uint4*>(src + ((lane & 7) + 8 * i) * 16)) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int row = 32 * y + warp * 4 + (lane >> 3), qp = lane & 7;
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < 9; ++i) {
+          const uint32_t v[4] = {qr[y][i].x, qr[y][i].y, qr[y][i].z, qr[y][i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = k8_two(v[j], a.f16);
+            big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, d));
+        const int E = big > 0.f ? max((int)(__float_as_uint(big) >> 23) - 127, -110) : 14;
+        const float mul = __uint_as_float((uint32_t)(14 - E + 127) << 23);
+        if (qp == 0) head_of[row] = make_float2(a.scale_log2 * __uint_as_float((uint32_t)(E - 14 + 127) << 23), 0.f);
+#pragma unroll
+        for (int i = 0; i < 9; ++i) {
+          const uint32_t v[4] = {qr[y][i].x, qr[y][i].y, qr[y][i].z, qr[y][i].w};
+          uint32_t hv[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = k8_two(v[j], a.f16);
+            hv[j] = k8_halves(f.x * mul, f.y * mul);
+          }
+          *reinterpret_cast<uint4*>(smem + P::kQAt + i * 8192 + row * 128 + ((qp ^ (row & 7)) << 4)) =
+              make_uint4(hv[0], hv[1], hv[2], hv[3]);
+        }
+      }
+
+      float l[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) l[i] = 0.f;
+      bool first = true;
+      for (int k = 0; k < n_steps; ++k, ++n) {
+        const uint32_t ph = (uint32_t)(n & 1);
+        // --- codes to halves, slab by slab ---
+        if (lane < 16) {
+          see_of[ph * kTcRows + warp * 16 + lane] = see_next;
+          scale_of[ph * kTcRows + warp * 16 + lane] = ks_next;
+        }
+        point(next_row, next_page);
+        next_row = resolve(k + 2, next_x);
+        next_page = fetch_page(next_row);
+        next_x = fetch_idx(k + 3);
+#pragma unroll
+        for (int sl = 0; sl < 9; ++sl) {
+          if (n > 0 && (sl & 1) == 0 && sl < 8 && !dead) dead = !mbar_wait(blk_free + (sl >> 1), ph ^ 1, &abort_word, c.status);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int r = warp * 16 + 8 * j + (lane >> 2), ch = 2 * (lane & 3);
+            uint32_t w[8];
+            k8_pair<FMT>(raw[sl][j].x, w[0], w[1]);
+            k8_pair<FMT>(raw[sl][j].y, w[2], w[3]);
+            k8_pair<FMT>(raw[sl][j].z, w[4], w[5]);
+            k8_pair<FMT>(raw[sl][j].w, w[6], w[7]);
+            uint8_t* dst = smem + sl * kTcSlab + r * 128;
+            *reinterpret_cast<uint4*>(dst + ((ch ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full + sl);
+        }
+        // the next chunk's codes: behind the fences, which wait for what is on its way
+#pragma unroll
+        for (int sl = 0; sl < 9; ++sl)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            raw[sl][j] = ptr[j] ? __ldg(reinterpret_cast<const uint4*>(ptr[j] + sl * 64)) : make_uint4(0, 0, 0, 0);
+        tc_bar();  // the chunk's rows and scales, and Q's factors, are there for all
+
+        // --- softmax: this thread's row against 32 heads ---
+        const bool see = see_of[ph * kTcRows + row_j] != 0;
+        const float ks = k8_scale(scale_of[ph * kTcRows + row_j]), lv = k8_log2(ks), iv = k8_rcp(ks);
+        if (!dead) dead = !mbar_wait(s_done, ph, &abort_word, c.status);
+        tc_fence_after();
+        float s[32];
+        {
+          uint32_t r0[16], r1[16];
+          tmem_ld16(tm_lane + P::kTmemS + 32 * hh, r0);
+          tmem_ld16(tm_lane + P::kTmemS + 32 * hh + 16, r1);
+          tmem_wait_ld();
+          reg_dep16(r0);
+          reg_dep16(r1);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            s[i] = __uint_as_float(r0[i]);
+            s[16 + i] = __uint_as_float(r1[i]);
+          }
+        }
+        const float4* hf = reinterpret_cast<const float4*>(head_of + 32 * hh);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float4 f = hf[i];
+          s[2 * i] = see ? fmaf(s[2 * i], f.x * ks, lv - f.y) : -INFINITY;
+          s[2 * i + 1] = see ? fmaf(s[2 * i + 1], f.z * ks, lv - f.w) : -INFINITY;
+          mx = fmaxf(mx, fmaxf(s[2 * i], s[2 * i + 1]));
+        }
+        if (tc_any(mx > (first ? -INFINITY : kK8Top + kK8Grow))) {
+          // the chunk's maxima per head: over the warp's rows, then over the four warps
+          float mine = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            // floats in the order of signed integers; NaN as -inf
+            const int b = __float_as_int(s[i]), key = b >= 0 ? b : b ^ 0x7fffffff;
+            const int top = __reduce_max_sync(~0u, s[i] == s[i] ? key : (int)0x807fffff);
+            if (lane == i) mine = __int_as_float(top >= 0 ? top : top ^ 0x7fffffff);
+          }
+          red[(warp & 3) * 64 + 32 * hh + lane] = mine;
+          tc_bar();
+          if (tid < 64) {
+            const float v = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid]));
+            const float d = v > (first ? -INFINITY : kK8Top + kK8Grow) ? v - kK8Top : 0.f;
+            red[tid] = d;
+            head_of[tid].y += d;
+          }
+          tc_bar();
+          const float* shift = red + 32 * hh;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float d = shift[i];
+            s[i] -= d;
+            if (!first) l[i] *= ex2_approx(-d);
+          }
+          if (!first) {
+            // O^T's blocks 2 hh and 2 hh + 1, 16 columns (heads) at a time
+            const unsigned long long moved = __ballot_sync(~0u, red[lane] != 0.f) |
+                                             (unsigned long long)__ballot_sync(~0u, red[32 + lane] != 0.f) << 32;
+#pragma unroll 1
+            for (int cb = 0; cb < 128; cb += 16) {
+              if (!((moved >> (cb & 63)) & 0xffff)) continue;  // none of these heads grew
+              uint32_t r[16];
+              const uint32_t at = tm_lane + hh * 128 + cb;
+              tmem_ld16(at, r);
+              tmem_wait_ld();
+              reg_dep16(r);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * ex2_approx(-red[(cb + i) & 63]));
+              tmem_st16(at, r);
+            }
+            tmem_wait_st();
+          }
+          first = false;
+          tc_bar();  // red is written again by the next exchange
+        }
+        if (tid == 0) fresh = k == 0;
+        // --- P^T: row j of the last slab, 64 heads of 2 bytes ---
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float e0 = ex2_approx(s[8 * i + 2 * j]), e1 = ex2_approx(s[8 * i + 2 * j + 1]);
+            l[8 * i + 2 * j] = fmaf(e0, iv, l[8 * i + 2 * j]);
+            l[8 * i + 2 * j + 1] = fmaf(e1, iv, l[8 * i + 2 * j + 1]);
+            w[j] = k8_halves(e0, e1);
+          }
+          *reinterpret_cast<uint4*>(smem + 8 * kTcSlab + row_j * 128 + (((4 * hh + i) ^ (row_j & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+      }
+
+      // --- the part's sums, and O^T out ---
+      if (!dead) dead = !mbar_wait(blk_free + 3, (uint32_t)((n - 1) & 1), &abort_word, c.status);
+      tc_fence_after();
+#pragma unroll
+      for (int d = 16; d; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < d; ++i) {
+          const float keep = lane & d ? l[i + d] : l[i], give = lane & d ? l[i] : l[i + d];
+          l[i] = keep + __shfl_xor_sync(~0u, give, d);
+        }
+      red[(warp & 3) * 64 + 32 * hh + lane] = l[0];  // lane x holds head x's
+      tc_bar();
+      const bool whole = u.c0 == 0 && u.c1 == u.ch;
+      float norm = 0.f;
+      if (tid < u.rows) {
+        const float m = first ? -INFINITY : head_of[tid].y + kK8Top;
+        const float total =
+            dead ? __int_as_float(0x7fffffff) : red[tid] + red[64 + tid] + red[128 + tid] + red[192 + tid];
+        if (whole) {
+          float lse;
+          norm = k8_norm(k8_sink(a, u.head0 + tid), m, total, &lse);
+          a.lse[(long long)u.t0 * a.Hq + u.head0 + tid] = lse;
+        } else {
+          part_out[tid] = m;
+          part_out[64 + tid] = total;
+        }
+      }
+      tc_bar();
+      if (tid < 64) red[tid] = norm;
+      tc_bar();
+#pragma unroll 1
+      for (int mb = 2 * hh; mb < 2 * hh + 2; ++mb) {
+        const int d = mb * 128 + row_j;
+        char* const out = static_cast<char*>(a.o) + (((long long)u.t0 * a.Hq + u.head0) * kLatDV + d) * 2;
+        float* const part = part_out + 128 + d;
+#pragma unroll 1
+        for (int h0 = 0; h0 < u.rows; h0 += 32) {
+          uint32_t r0[16], r1[16];
+          tmem_ld16(tm_lane + mb * 64 + h0, r0);
+          tmem_ld16(tm_lane + mb * 64 + h0 + 16, r1);
+          tmem_wait_ld();
+          reg_dep16(r0);
+          reg_dep16(r1);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (h0 + i < u.rows) {
+              const float v = __uint_as_float(i < 16 ? r0[i & 15] : r1[i & 15]);
+              if (whole) {
+                const float f = red[h0 + i], y = f == 0.f ? 0.f : v * f;
+                const uint32_t w = a.f16 ? k8_halves(y, 0.f) : pack_bf16(y, 0.f);
+                *reinterpret_cast<unsigned short*>(out + (h0 + i) * kLatDV * 2) = (unsigned short)w;
+              } else {
+                part[(h0 + i) * kLatDV] = v;
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      if (!whole && tid == 0) k8_note(ws, cur.share, u.begin, u.c0, u.ch, u.t0, u.head0, u.rows, a.gdiv);
+      part_out = k8_part(ws, gridDim.x, 2 * blockIdx.x + 1, 64, kLatDV);
+      tc_bar();  // red and Q's factors are written again
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
 template <int MT, int FMT>
 static cudaError_t latent_t(const K8Fwd& a, void* ws, cudaStream_t st) {
   using P = K8Lat<MT>;
@@ -1452,19 +1882,28 @@ template <int FMT>
 static cudaError_t latent_f(const K8Fwd& a, void* ws, cudaStream_t st) {
   if (a.unit_rows == 16) return latent_t<1, FMT>(a, ws, st);
   if (a.unit_rows == 32) return latent_t<2, FMT>(a, ws, st);
-  return latent_t<4, FMT>(a, ws, st);
+  static unsigned long long done = 0;
+  cudaError_t e = allow_smem(k8_tc_kernel<FMT>, K8Tc::kSmem, done);
+  if (e != cudaSuccess) return e;
+  const int n = k8_ctas(a);
+  count_launch();
+  e = launch_pdl(k8_tc_kernel<FMT>, (unsigned)n, 384, K8Tc::kSmem, st, a, static_cast<float*>(ws));
+  if (e != cudaSuccess || n == 1) return e;
+  count_launch();
+  return launch_pdl(k8_join_kernel<64, kLatDV>, (unsigned)n, 256, 0, st, a, static_cast<float*>(ws), n);
 }
 
 static void k8_geometry(K8Fwd& a) {
   const bool lat = k8_latent(a);
-  a.chunk = lat ? kLatRows : kK8Chunk;
   a.unit_rows = !lat ? 16 : a.G <= 16 ? 16 : a.G <= 32 ? 32 : 64;
+  a.chunk = !lat ? kK8Chunk : a.unit_rows == 64 ? kTcRows : kLatRows;
   a.gdiv = min(a.G, a.unit_rows);
   a.hs = (a.G + a.unit_rows - 1) / a.unit_rows;
   a.tpt = lat || a.topk || a.G > 16 ? 1 : 16 / a.G;
   a.sel_ch = a.topk ? (int)(((long long)a.topk * a.bs + a.chunk - 1) / a.chunk) : 0;
   a.by_tpt = k8_div_of(a.tpt);
   a.by_gdiv = k8_div_of(a.gdiv);
+  a.whole_units = a.unit_rows == 64;
 }
 
 size_t k8_fwd_workspace(K8Fwd a) {
