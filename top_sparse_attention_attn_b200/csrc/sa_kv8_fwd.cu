@@ -1458,7 +1458,7 @@ struct K8Tc {
   static constexpr int kMetaAt = kQAt + 9 * 64 * 128;       // [2][128] rows seen, [2][128] scales
   static constexpr int kHeadAt = kMetaAt + 2 * kTcRows * 8;  // [64] (fr, base)
   static constexpr int kRedAt = kHeadAt + 64 * 8;            // [4][64]
-  static constexpr int kBarAt = kRedAt + 4 * 64 * 4;         // full [9], p_full, s_done, free [4]
+  static constexpr int kBarAt = kRedAt + 4 * 64 * 4;         // full [4], p_full, s_done, free [4]
   static constexpr int kSmem = kBarAt + 16 * 8 + 1024;
   static constexpr uint32_t kTmemS = 256;  // column of S^T behind the four blocks of O^T
 };
@@ -1489,10 +1489,10 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
   const K8Cache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + P::kBarAt);
-  uint64_t *const p_full = full + 9, *const s_done = full + 10, *const blk_free = full + 11;
+  uint64_t *const p_full = full + 4, *const s_done = full + 5, *const blk_free = full + 6;
   if (tid == 0) {
-    for (int i = 0; i < 10; ++i) mbar_init(full + i, 8);
-    for (int i = 10; i < 15; ++i) mbar_init(full + i, 1);
+    for (int i = 0; i < 5; ++i) mbar_init(full + i, 8);
+    for (int i = 5; i < 10; ++i) mbar_init(full + i, 1);
     mbar_fence_init();
     abort_word = 0;
   }
@@ -1523,13 +1523,16 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
         const uint32_t ph = (uint32_t)(n & 1);
         bool ok = true;
 #pragma unroll 1
-        for (int sl = 0; sl < kTcSlabs && ok; ++sl) {
-          ok = mbar_wait(full + sl, ph, &abort_word, c.status);
+        for (int g = 0; g < 4; ++g) {  // slabs 2 g and 2 g + 1, the ninth with the last
+          ok = mbar_wait(full + g, ph, &abort_word, c.status);
           tc_fence_after();
           if (!ok) break;
-          const uint64_t A = desc_add(dk, sl * kTcSlab), B = desc_add(dq, sl * 8192);
+          const uint64_t A = desc_add(dk, g * 2 * kTcSlab), B = desc_add(dq, g * 2 * 8192);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mma_bf16(tmem + P::kTmemS, desc_add(A, 32 * e), desc_add(B, 32 * e), id_s, sl || e);
+          for (int e = 0; e < 12; ++e)
+            if (e < 8 || g == 3)
+              mma_bf16(tmem + P::kTmemS, desc_add(A, (e >> 2) * kTcSlab + 32 * (e & 3)),
+                       desc_add(B, (e >> 2) * 8192 + 32 * (e & 3)), id_s, g || e);
         }
         if (!ok) break;
         mma_commit(s_done);
@@ -1685,9 +1688,11 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
             *reinterpret_cast<uint4*>(dst + ((ch ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
           }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(full + sl);
+          if (((sl & 1) && sl < 7) || sl == 8) {  // a pair of slabs (a fence costs some 300 cycles)
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full + (sl < 8 ? sl >> 1 : 3));
+          }
         }
         // the next chunk's codes: behind the fences, which wait for what is on its way
 #pragma unroll
