@@ -1478,6 +1478,22 @@ __device__ __forceinline__ bool tc_any(bool x) {
   return r != 0;
 }
 
+struct K8Codes {
+  uint32_t w[8];
+};
+__device__ __forceinline__ K8Codes tc_ld32(const uint8_t* p) {  // 32 codes, 32-byte aligned; none: zeros
+  K8Codes r;
+  if (p) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
+                   "=r"(r.w[7])
+                 : "l"(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.w[i] = 0;
+  }
+  return r;
+}
 template <int FMT>
 __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K8Fwd a, float* ws) {
   using P = K8Tc;
@@ -1589,7 +1605,7 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
       };
       auto fetch_page = [&](int row) -> int { return row >= 0 ? __ldg(u.table + k8_quot(c.by_ps, row)) : 0; };
       // the lane's two rows of the codes and its row's scale, from what was looked up
-      const uint8_t* ptr[2];
+      const uint8_t* ptr[3];  // pairs of slabs: rows 8 j + lane / 4, 32 codes of 128; the ninth: row lane / 2
       float ks_next = 0.f;
       bool see_next = false;
       auto point = [&](int row, int page) {
@@ -1601,22 +1617,13 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
         see_next = row >= 0;
         if (see_next) ks_next = __ldg(c.ks + (long long)page * c.Hkv + u.h);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int at = __shfl_sync(~0u, rr, 8 * j + (lane >> 2));
-          ptr[j] = at >= 0 ? c.k + (long long)at * krs + u.h * kLatDK + (lane & 3) * 16 : nullptr;
+        for (int j = 0; j < 3; ++j) {
+          const int at = __shfl_sync(~0u, rr, j < 2 ? 8 * j + (lane >> 2) : lane >> 1);
+          const int col = j < 2 ? (lane & 3) * 32 : 512 + (lane & 1) * 32;
+          ptr[j] = at >= 0 ? c.k + (long long)at * krs + u.h * kLatDK + col : nullptr;
         }
       };
       int x0 = fetch_idx(0), x1 = fetch_idx(1), next_x = fetch_idx(2);
-      const int row0 = resolve(0, x0), pg0 = fetch_page(row0);
-      int next_row = resolve(1, x1), next_page = fetch_page(next_row);
-      uint4 raw[9][2];
-      point(row0, pg0);
-#pragma unroll
-      for (int sl = 0; sl < 9; ++sl)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          raw[sl][j] = ptr[j] ? __ldg(reinterpret_cast<const uint4*>(ptr[j] + sl * 64)) : make_uint4(0, 0, 0, 0);
-
       // --- Q, 8 lanes a row, as halves times 2^(14 - E); the scores of the unit before have been taken ---
       uint4 qr[2][9];
 #pragma unroll
@@ -1627,6 +1634,16 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
         for (int i = 0; i < 9; ++i)
           qr[y][i] = row < u.rows ? __ldg(reinterpret_cast<const uint4*>(src + ((lane & 7) + 8 * i) * 16)) : make_uint4(0, 0, 0, 0);
       }
+      const int row0 = resolve(0, x0), pg0 = fetch_page(row0);
+      int next_row = resolve(1, x1), next_page = fetch_page(next_row);
+      K8Codes raw[9];  // pair g, row j: 2 g + j
+      auto load_codes = [&]() {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) raw[x] = tc_ld32(ptr[x & 1] ? ptr[x & 1] + (x >> 1) * 128 : nullptr);
+        raw[8] = tc_ld32(ptr[2]);
+      };
+      point(row0, pg0);
+      load_codes();
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int row = 32 * y + warp * 4 + (lane >> 3), qp = lane & 7;
@@ -1671,36 +1688,39 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
           scale_of[ph * kTcRows + warp * 16 + lane] = ks_next;
         }
         point(next_row, next_page);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)  // 8 rows of 576 bytes: 4 lanes a row, 128 bytes apart, and the last 64
+          if (ptr[j]) {
+            asm volatile("prefetch.global.L2 [%0];\n" ::"l"(ptr[j] + (lane & 3) * 96));  // 128 apart
+            if ((lane & 3) == 0) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(ptr[j] + 544));
+          }
         next_row = resolve(k + 2, next_x);
         next_page = fetch_page(next_row);
         next_x = fetch_idx(k + 3);
+        // 32 codes to 64 bytes of slab `sl`, row r, from its 16-byte piece ch0 on.  The order of the pieces
+        // keeps eight lanes' stores (two rows, two slabs) on different banks.
+        auto put = [&](const K8Codes& x, int sl, int r, int ch0, int turn) {
+          uint8_t* dst = smem + sl * kTcSlab + r * 128;
 #pragma unroll
-        for (int sl = 0; sl < 9; ++sl) {
-          if (n > 0 && (sl & 1) == 0 && sl < 8 && !dead) dead = !mbar_wait(blk_free + (sl >> 1), ph ^ 1, &abort_word, c.status);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int r = warp * 16 + 8 * j + (lane >> 2), ch = 2 * (lane & 3);
-            uint32_t w[8];
-            k8_pair<FMT>(raw[sl][j].x, w[0], w[1]);
-            k8_pair<FMT>(raw[sl][j].y, w[2], w[3]);
-            k8_pair<FMT>(raw[sl][j].z, w[4], w[5]);
-            k8_pair<FMT>(raw[sl][j].w, w[6], w[7]);
-            uint8_t* dst = smem + sl * kTcSlab + r * 128;
-            *reinterpret_cast<uint4*>(dst + ((ch ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(dst + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+          for (int y = 0; y < 4; ++y) {
+            const int i = y ^ turn;  // 0 or 2: the words below are picked by selects
+            uint32_t w[4];
+            k8_pair<FMT>(turn ? x.w[2 * (y ^ 2)] : x.w[2 * y], w[0], w[1]);
+            k8_pair<FMT>(turn ? x.w[2 * (y ^ 2) + 1] : x.w[2 * y + 1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + (((ch0 + i) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          if (((sl & 1) && sl < 7) || sl == 8) {  // a pair of slabs (a fence costs some 300 cycles)
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full + (sl < 8 ? sl >> 1 : 3));
-          }
-        }
-        // the next chunk's codes: behind the fences, which wait for what is on its way
+        };
 #pragma unroll
-        for (int sl = 0; sl < 9; ++sl)
+        for (int g = 0; g < 4; ++g) {
+          if (n > 0 && !dead) dead = !mbar_wait(blk_free + g, ph ^ 1, &abort_word, c.status);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            raw[sl][j] = ptr[j] ? __ldg(reinterpret_cast<const uint4*>(ptr[j] + sl * 64)) : make_uint4(0, 0, 0, 0);
+            put(raw[2 * g + j], 2 * g + ((lane >> 1) & 1), warp * 16 + 8 * j + (lane >> 2), 4 * (lane & 1), lane & 2);
+          if (g == 3) put(raw[8], 8, warp * 16 + (lane >> 1), 4 * (lane & 1), 0);
+          fence_async_smem();  // costs some 300 cycles: once for a pair of slabs
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full + g);
+        }
         tc_bar();  // the chunk's rows and scales, and Q's factors, are there for all
 
         // --- softmax: this thread's row against 32 heads ---
@@ -1797,6 +1817,8 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
+        // the next chunk's codes, from L2 by now: behind this chunk's fences, which would wait for them
+        if (k + 1 < n_steps) load_codes();
       }
 
       // --- the part's sums, and O^T out ---
@@ -1842,18 +1864,24 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
           tmem_wait_ld();
           reg_dep16(r0);
           reg_dep16(r1);
+          if (whole) {
+            // two heads at a time: even lanes store columns d, d + 1 of the first, odd ones d - 1, d of the second
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (h0 + i < u.rows) {
-              const float v = __uint_as_float(i < 16 ? r0[i & 15] : r1[i & 15]);
-              if (whole) {
-                const float f = red[h0 + i], y = f == 0.f ? 0.f : v * f;
-                const uint32_t w = a.f16 ? k8_halves(y, 0.f) : pack_bf16(y, 0.f);
-                *reinterpret_cast<unsigned short*>(out + (h0 + i) * kLatDV * 2) = (unsigned short)w;
-              } else {
-                part[(h0 + i) * kLatDV] = v;
-              }
+            for (int i = 0; i < 32; i += 2) {
+              const float f0 = red[h0 + i], f1 = red[h0 + i + 1];
+              const float v0 = __uint_as_float(i < 16 ? r0[i & 15] : r1[i & 15]);
+              const float v1 = __uint_as_float(i < 16 ? r0[(i + 1) & 15] : r1[(i + 1) & 15]);
+              const float y0 = f0 == 0.f ? 0.f : v0 * f0, y1 = f1 == 0.f ? 0.f : v1 * f1;
+              const bool odd = lane & 1;
+              const float got = __shfl_xor_sync(~0u, odd ? y0 : y1, 1), lo = odd ? got : y0, hi = odd ? y1 : got;
+              const int head = h0 + i + odd;
+              if (head < u.rows)
+                *reinterpret_cast<uint32_t*>(out + (head * kLatDV - odd) * 2) = a.f16 ? k8_halves(lo, hi) : pack_bf16(lo, hi);
             }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (h0 + i < u.rows) part[(h0 + i) * kLatDV] = __uint_as_float(i < 16 ? r0[i & 15] : r1[i & 15]);
           }
         }
       }
@@ -1901,7 +1929,8 @@ static cudaError_t latent_f(const K8Fwd& a, void* ws, cudaStream_t st) {
 
 static void k8_geometry(K8Fwd& a) {
   const bool lat = k8_latent(a);
-  a.unit_rows = !lat ? 16 : a.G <= 16 ? 16 : a.G <= 32 ? 32 : 64;
+  // (the tcgen05 kernel reads codes 32 bytes at a time)
+  a.unit_rows = !lat ? 16 : a.G <= 16 ? 16 : a.G <= 32 || ((uintptr_t)a.c.k & 31) ? 32 : 64;
   a.chunk = !lat ? kK8Chunk : a.unit_rows == 64 ? kTcRows : kLatRows;
   a.gdiv = min(a.G, a.unit_rows);
   a.hs = (a.G + a.unit_rows - 1) / a.unit_rows;
