@@ -1637,13 +1637,17 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
       const int row0 = resolve(0, x0), pg0 = fetch_page(row0);
       int next_row = resolve(1, x1), next_page = fetch_page(next_row);
       K8Codes raw[9];  // pair g, row j: 2 g + j
-      auto load_codes = [&]() {
+      auto load_a = [&]() {
 #pragma unroll
-        for (int x = 0; x < 8; ++x) raw[x] = tc_ld32(ptr[x & 1] ? ptr[x & 1] + (x >> 1) * 128 : nullptr);
+        for (int x = 0; x < 4; ++x) raw[x] = tc_ld32(ptr[x & 1] ? ptr[x & 1] + (x >> 1) * 128 : nullptr);
+      };
+      auto load_b = [&]() {
+#pragma unroll
+        for (int x = 4; x < 8; ++x) raw[x] = tc_ld32(ptr[x & 1] ? ptr[x & 1] + (x >> 1) * 128 : nullptr);
         raw[8] = tc_ld32(ptr[2]);
       };
       point(row0, pg0);
-      load_codes();
+      load_a(); load_b();
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int row = 32 * y + warp * 4 + (lane >> 3), qp = lane & 7;
@@ -1721,6 +1725,7 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
           __syncwarp();
           if (lane == 0) mbar_arrive(full + g);
         }
+        if (k + 1 < n_steps) load_a();
         tc_bar();  // the chunk's rows and scales, and Q's factors, are there for all
 
         // --- softmax: this thread's row against 32 heads ---
@@ -1818,7 +1823,7 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
         // the next chunk's codes, from L2 by now: behind this chunk's fences, which would wait for them
-        if (k + 1 < n_steps) load_codes();
+        if (k + 1 < n_steps) load_b();
       }
 
       // --- the part's sums, and O^T out ---
