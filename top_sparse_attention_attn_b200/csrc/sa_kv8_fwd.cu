@@ -245,6 +245,15 @@ __device__ __forceinline__ K8Span k8_span(const K8Fwd& a, int b) {
   return r;
 }
 
+// a / b for 0 <= a < 2^31, 1 <= b: an approximate quotient, then put right (an exact division is a chain
+// of some hundred dependent instructions, in front of everything else here).
+__device__ __forceinline__ uint32_t k8_udiv(uint32_t a, uint32_t b) {
+  uint32_t q = (uint32_t)__fdividef((float)a, (float)b);
+  while (q * (unsigned long long)b > a) --q;
+  while ((q + 1ull) * b <= a) ++q;
+  return q;
+}
+
 // Where a CTA stands on the line.
 struct K8Cursor {
   long long w0, w1;  // its share
@@ -293,7 +302,7 @@ __device__ __forceinline__ bool k8_begin(const K8Fwd& a, float* ws, int tid, K8F
   if (tid < 2) (reinterpret_cast<K8Join*>(ws) + 2 * blockIdx.x)[tid].n = 0;
   if (blockIdx.x >= n_cta) return false;
   if (W <= 0x7fffffff) {
-    cur.share.base = (uint32_t)W / (uint32_t)n_cta;
+    cur.share.base = k8_udiv((uint32_t)W, (uint32_t)n_cta);
     cur.share.rem = (int)((uint32_t)W - (uint32_t)cur.share.base * (uint32_t)n_cta);
   } else {
     cur.share.base = W / n_cta;
@@ -307,11 +316,11 @@ __device__ __forceinline__ bool k8_begin(const K8Fwd& a, float* ws, int tid, K8F
       const long long n = (long long)sp.units * sp.ch;
       if (cur.w0 < at + n) {
         const long long off = cur.w0 - at;
-        const int unit = off <= 0x7fffffff ? (int)((uint32_t)off / (uint32_t)sp.ch) : (int)(off / sp.ch);
+        const int unit = off <= 0x7fffffff ? (int)k8_udiv((uint32_t)off, (uint32_t)sp.ch) : (int)(off / sp.ch);
         f.at = at;
         f.sp = sp;
         f.b = b;
-        f.h = (uint32_t)unit / (uint32_t)sp.per_h;
+        f.h = (int)k8_udiv((uint32_t)unit, (uint32_t)sp.per_h);
         f.ut = unit - f.h * sp.per_h;
         f.c0 = (int)(off - (long long)unit * sp.ch);
         break;
@@ -404,10 +413,6 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
   if (!ROWS) {
     if (lane < S) mbar_init(bars + lane, 1);
     mbar_fence_init();
-    if (tid == 0) {
-      tma_prefetch_desc(&maps.k);
-      tma_prefetch_desc(&maps.v);
-    }
   }
   pdl_trigger();  // the join waits for this kernel's end, but need not be launched after it
   pdl_wait();
