@@ -56,6 +56,7 @@ struct K8Fwd {
   // most, tokens per unit, query rows of a token in a unit, units over a token's heads, and
   // chunks of a unit that selects (0: every row)
   int chunk, unit_rows, tpt, gdiv, hs, sel_ch;
+  int over, keep;   // see k8_begin
   int whole_units;  // rather a CTA per unit than parts, where that is nearly as even
   K8Div by_tpt, by_gdiv;
   int win;           // rows before the token's own that it sees (INT_MAX: all)

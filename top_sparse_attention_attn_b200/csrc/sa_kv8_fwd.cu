@@ -172,12 +172,11 @@ __device__ __forceinline__ void k8_copy_rows(uint32_t dst, const uint8_t* src, i
 struct K8Join {
   int n;      // CTAs that hold a part of the unit; 0: nothing to join
   int first;  // the first of them
-  int slot;   // where its part lies (the others' lies in slot 0)
   int t, head, rows, gdiv;
 };
 // The workspace: two K8Join per CTA (the unit in whose midst its share begins; the unit
-// that begins in its share and ends behind it), then two parts per CTA, slot 0 the one
-// that its share begins with: maxima and sums of a unit's rows (16, or 16 MT), and O [rows][DV].
+// that begins in its share and ends behind it), then these units' parts, two per CTA:
+// maxima and sums of a unit's rows (16, or 16 MT), and O [rows][DV].
 __host__ __device__ inline size_t k8_parts_at(int n_cta) {
   return ((size_t)n_cta * 2 * sizeof(K8Join) + 255) / 256 * 256;
 }
@@ -229,6 +228,7 @@ struct K8Span {
   K8Seq s;
   int units, ch;
   int per_h;  // units of a KV head
+  int len;    // a unit on the line: its chunks, and a.over for what a unit costs besides
 };
 __device__ __forceinline__ K8Span k8_span(const K8Fwd& a, int b) {
   K8Span r;
@@ -242,6 +242,7 @@ __device__ __forceinline__ K8Span k8_span(const K8Fwd& a, int b) {
     // a window: from the step of 16 that its first row lies in
     if (a.win < (1 << 29)) r.ch = min(r.ch, (a.win + a.tpt + 15 + a.chunk - 1) / a.chunk);
   }
+  r.len = r.ch + a.over;
   return r;
 }
 
@@ -264,7 +265,7 @@ struct K8Cursor {
 };
 struct K8Found {
   long long sum[8];
-  long long at;
+  long long at, w0, w1;
   int b, h, ut, c0;
   K8Span sp;
 };
@@ -278,7 +279,7 @@ __device__ __forceinline__ bool k8_begin(const K8Fwd& a, float* ws, int tid, K8F
   K8Span sp = {};
   for (int b = b0; b < b1; ++b) {
     sp = k8_span(a, b);
-    mine += (long long)sp.units * sp.ch;
+    mine += (long long)sp.units * sp.len;
   }
   long long inc = mine;
 #pragma unroll
@@ -308,38 +309,57 @@ __device__ __forceinline__ bool k8_begin(const K8Fwd& a, float* ws, int tid, K8F
     cur.share.base = W / n_cta;
     cur.share.rem = (int)(W % n_cta);
   }
-  cur.w0 = cur.share.at(blockIdx.x);
-  cur.w1 = cur.share.at(blockIdx.x + 1);
-  if (at <= cur.w0 && cur.w0 < at + mine) {
+  // This share's two ends, each put where a unit can be cut: not within its first a.over, and not at
+  // all in a unit of up to a.keep chunks while a CTA has such a unit or more.  (Both CTAs at
+  // an end see it alike.)
+  const long long ends[2] = {cur.share.at(blockIdx.x), cur.share.at(blockIdx.x + 1)};
+  if (tid == 0 && ends[1] >= W) f.w1 = W;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (!(at <= ends[e] && ends[e] < at + mine)) continue;
+    long long from = at;
     for (int b = b0;; ++b) {
       if (b1 - b0 > 1) sp = k8_span(a, b);
-      const long long n = (long long)sp.units * sp.ch;
-      if (cur.w0 < at + n) {
-        const long long off = cur.w0 - at;
-        const int unit = off <= 0x7fffffff ? (int)k8_udiv((uint32_t)off, (uint32_t)sp.ch) : (int)(off / sp.ch);
-        f.at = at;
+      const long long n = (long long)sp.units * sp.len;
+      if (ends[e] >= from + n) {
+        from += n;
+        continue;
+      }
+      const long long off = ends[e] - from;
+      const int unit = off <= 0x7fffffff ? (int)k8_udiv((uint32_t)off, (uint32_t)sp.len) : (int)(off / sp.len);
+      int pos = (int)(off - (long long)unit * sp.len);
+      if (sp.ch <= a.keep && cur.share.base >= sp.len) pos = 2 * pos < sp.len ? 0 : sp.len;
+      else if (pos <= a.over) pos = 0;
+      (e ? f.w1 : f.w0) = from + (long long)unit * sp.len + pos;
+      if (e == 0) {
+        f.at = from;
         f.sp = sp;
         f.b = b;
         f.h = (int)k8_udiv((uint32_t)unit, (uint32_t)sp.per_h);
         f.ut = unit - f.h * sp.per_h;
-        f.c0 = (int)(off - (long long)unit * sp.ch);
-        break;
+        f.c0 = pos == 0 || pos == sp.len ? 0 : pos - a.over;
+        if (pos == sp.len && ++f.ut == sp.per_h) {
+          f.ut = 0;
+          ++f.h;
+        }
       }
-      at += n;
+      break;
     }
   }
   __syncthreads();
+  cur.w0 = f.w0;
+  cur.w1 = f.w1;
   cur.seq_at = f.at;
   cur.sp = f.sp;
   cur.b = f.b;
   cur.h = f.h;
   cur.ut = f.ut;
   cur.c0 = f.c0;
-  return true;
+  return cur.w0 < cur.w1;
 }
 __device__ __forceinline__ void k8_settle(const K8Fwd& a, K8Cursor& c) {  // to the next sequence with work
   while (c.h >= a.c.Hkv || c.sp.units == 0) {
-    c.seq_at += (long long)c.sp.units * c.sp.ch;
+    c.seq_at += (long long)c.sp.units * c.sp.len;
     c.sp = k8_span(a, ++c.b);
     c.h = 0;
   }
@@ -351,20 +371,19 @@ __device__ __forceinline__ void k8_next(K8Cursor& c) {
     ++c.h;
   }
 }
-// Notes that this CTA leaves a part of a unit of `ch` chunks that begins at `begin`; c0: the part's first.
-__device__ __forceinline__ void k8_note(float* ws, const K8Share& share, long long begin, int c0, int ch, int t, int head,
-                                        int rows, int gdiv) {
+// Notes that this CTA leaves a part of a unit of length len that begins at `begin`; c0: the part's first chunk.
+__device__ __forceinline__ void k8_note(const K8Fwd& a, float* ws, const K8Share& share, long long begin, int c0, int len,
+                                        int t, int head, int rows, int gdiv) {
   K8Join jn;
-  jn.first = c0 == 0 ? (int)blockIdx.x : share.of(begin);
-  jn.n = share.of(begin + ch - 1) - jn.first + 1;
-  jn.slot = share.at(jn.first) == begin ? 0 : 1;
+  jn.first = c0 == 0 ? (int)blockIdx.x : share.of(begin + a.over);
+  jn.n = share.of(begin + len - 1) - jn.first + 1;
   jn.t = t;
   jn.head = head;
   jn.rows = rows;
   jn.gdiv = gdiv;
   (reinterpret_cast<K8Join*>(ws) + 2 * blockIdx.x)[c0 == 0] = jn;
 }
-// The unit at the cursor, which moves on; left: chunks left of the share.
+// The unit at the cursor, which moves on.
 __device__ __forceinline__ K8Unit k8_take(const K8Fwd& a, K8Cursor& cur) {
   k8_settle(a, cur);
   const K8Span& sp = cur.sp;
@@ -372,8 +391,8 @@ __device__ __forceinline__ K8Unit k8_take(const K8Fwd& a, K8Cursor& cur) {
   u.h = cur.h;
   u.c0 = cur.c0;
   u.ch = sp.ch;
-  u.c1 = (int)min((long long)sp.ch, cur.c0 + (cur.w1 - cur.w0));
-  u.begin = cur.seq_at + ((long long)cur.h * sp.per_h + cur.ut) * sp.ch;
+  u.c1 = (int)min((long long)sp.ch, cur.c0 + (cur.w1 - cur.w0) - (cur.c0 ? 0 : a.over));
+  u.begin = cur.seq_at + ((long long)cur.h * sp.per_h + cur.ut) * sp.len;
   // a KV head's units lie together, a token's parts of the heads innermost
   const int tile = a.hs == 1 ? cur.ut : cur.ut / a.hs, hp = cur.ut - tile * a.hs;
   u.t0 = sp.s.t0 + tile * a.tpt;
@@ -391,7 +410,7 @@ __device__ __forceinline__ K8Unit k8_take(const K8Fwd& a, K8Cursor& cur) {
   u.slots = a.topk;
   if (a.topk && a.topk_len) u.slots = min(u.slots, max(0, __ldg(a.topk_len + iu)));
   u.table = a.c.table + cur.b * a.c.tstride;
-  cur.w0 += u.c1 - u.c0;
+  cur.w0 += u.c1 - u.c0 + (u.c0 ? 0 : a.over);
   k8_next(cur);
   return u;
 }
@@ -420,7 +439,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
   __shared__ K8Found found;
   K8Cursor cur;
   if (!k8_begin<128>(a, ws, tid, found, cur)) return;
-  float* part_out = k8_part(ws, gridDim.x, 2 * blockIdx.x, 16, DV);  // slot 0: the part that the share begins with
+  long long left = cur.w1 - cur.w0;  // of the share
 
   uint8_t* const wsm = smem + warp * S * P::kData;
   uint32_t* const sq = reinterpret_cast<uint32_t*>(smem + P::kQAt);
@@ -597,12 +616,11 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
   lay_q();
   __syncthreads();
 
-  long long left = cur.share.at(blockIdx.x + 1) - cur.share.at(blockIdx.x);  // chunks of the share
   int at = 0;
   for (int un = 0; left > 0; un = (un + 1) & (P::kRing - 1)) {
     const K8Unit& u = units[un];
     const int n_steps = u.c1 - u.c0, ta0 = u.ta0;
-    left -= n_steps;
+    left -= n_steps + (u.c0 ? 0 : a.over);
     const int lo_last = max(0, ta0 + u.ntok - 1 - a.win);
     int ta[2], lo[2];  // of this thread's rows gr and gr + 8
 #pragma unroll
@@ -871,6 +889,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
         total = fmaf(meet[x][16 + row], mw[x], total);
       }
       const bool whole = u.c0 == 0 && u.c1 == u.ch;
+      float* const part_out = k8_part(ws, gridDim.x, 2 * blockIdx.x + (u.c0 == 0), 16, DV);
       if (row < u.rows) {
         const int tok = k8_quot(a.by_gdiv, row), t = u.t0 + tok, head = u.head0 + row - tok * a.gdiv;
         float lse, norm = 0.f;
@@ -896,10 +915,9 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
           part_out[16 + row] = total;
         }
       }
-      if (!whole && tid == 0) k8_note(ws, cur.share, u.begin, u.c0, u.ch, u.t0, u.head0, u.rows, a.gdiv);
+      if (!whole && tid == 0)
+        k8_note(a, ws, cur.share, u.begin, u.c0, u.ch + a.over, u.t0, u.head0, u.rows, a.gdiv);
     }
-    // slot 1: any later part
-    part_out = k8_part(ws, gridDim.x, 2 * blockIdx.x + 1, 16, DV);
     if (left > 0) lay_q();  // every warp has taken the scores of this unit
     fence_async_smem();     // the copies that fill the stage again come behind these accesses
     __syncthreads();
@@ -921,6 +939,7 @@ __global__ void __launch_bounds__(256) k8_join_kernel(const K8Fwd a, float* ws, 
   constexpr int NV = DV < 128 ? 1 : DV / 128, kLanes = DV < 128 ? DV / 4 : 32;  // float4 of a lane, lanes
   __shared__ float sl[8];
   __shared__ float4 so[8][NV * kLanes];
+  pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll 1
@@ -928,7 +947,7 @@ __global__ void __launch_bounds__(256) k8_join_kernel(const K8Fwd a, float* ws, 
     const K8Join jn = reinterpret_cast<const K8Join*>(ws)[2 * blockIdx.x + which];
     if (jn.n == 0) continue;
     const int step = jn.n <= 8 ? 1 : 8, mine = blockIdx.x - jn.first;
-    auto part = [&](int x) { return k8_part(ws, n_grid, 2 * (jn.first + x) + (x ? 0 : jn.slot), R, DV); };
+    auto part = [&](int x) { return k8_part(ws, n_grid, 2 * (jn.first + x) + (x == 0), R, DV); };
     for (int row = mine + (step == 1 ? warp * jn.n : 0); row < jn.rows; row += step == 1 ? 8 * jn.n : jn.n) {
       const int head = jn.head + row % jn.gdiv;
       const float sink = k8_sink(a, head);
@@ -1088,7 +1107,6 @@ __global__ void __launch_bounds__(256, 1) k8_latent_kernel(const __grid_constant
   pdl_trigger();
   K8Cursor cur;
   if (!k8_begin<256>(a, ws, tid, found, cur)) return;
-  float* const parts = k8_part(ws, gridDim.x, 2 * blockIdx.x, R, kLatDV);
   const int krs = c.Hkv * kLatDK;
 
   for (long long w = cur.w0; w < cur.w1;) {
@@ -1406,7 +1424,7 @@ __global__ void __launch_bounds__(256, 1) k8_latent_kernel(const __grid_constant
       }
     __syncthreads();
     const bool whole = c0 == 0 && c1 == sp.ch;
-    float* part_out = parts + (w == cur.w0 ? 0 : k8_part_floats(R, kLatDV));
+    float* const part_out = k8_part(ws, gridDim.x, 2 * blockIdx.x + (c0 == 0), R, kLatDV);
 #pragma unroll
     for (int x = 0; x < MT; ++x)
 #pragma unroll
@@ -1436,7 +1454,8 @@ __global__ void __launch_bounds__(256, 1) k8_latent_kernel(const __grid_constant
         }
       }
     if (!whole && tid == 0)
-      k8_note(ws, cur.share, cur.seq_at + ((long long)cur.h * sp.per_h + cur.ut) * sp.ch, c0, sp.ch, t, head0, rows, a.gdiv);
+      k8_note(a, ws, cur.share, cur.seq_at + ((long long)cur.h * sp.per_h + cur.ut) * sp.len, c0, sp.len, t, head0, rows,
+              a.gdiv);
     __syncthreads();  // red, q_scale, the stages and Q are written again
     w += c1 - c0;
     k8_next(cur);
@@ -1581,7 +1600,6 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
     const uint32_t tm_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const int hh = warp >> 2, row_j = 32 * (warp & 3) + lane;  // this thread's heads and row in the softmax
     const int krs = c.Hkv * kLatDK;
-    float* part_out = k8_part(ws, gridDim.x, 2 * blockIdx.x, 64, kLatDV);
     bool dead = false;
     long long n = 0;  // chunks done
     while (n < n_chunks) {
@@ -1844,6 +1862,7 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
       red[(warp & 3) * 64 + 32 * hh + lane] = l[0];  // lane x holds head x's
       tc_bar();
       const bool whole = u.c0 == 0 && u.c1 == u.ch;
+      float* const part_out = k8_part(ws, gridDim.x, 2 * blockIdx.x + (u.c0 == 0), 64, kLatDV);
       float norm = 0.f;
       if (tid < u.rows) {
         const float m = first ? -INFINITY : head_of[tid].y + kK8Top;
@@ -1896,8 +1915,7 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
         }
       }
       tc_fence_before();
-      if (!whole && tid == 0) k8_note(ws, cur.share, u.begin, u.c0, u.ch, u.t0, u.head0, u.rows, a.gdiv);
-      part_out = k8_part(ws, gridDim.x, 2 * blockIdx.x + 1, 64, kLatDV);
+      if (!whole && tid == 0) k8_note(a, ws, cur.share, u.begin, u.c0, u.ch, u.t0, u.head0, u.rows, a.gdiv);
       tc_bar();  // red and Q's factors are written again
     }
   }
@@ -1949,6 +1967,9 @@ static void k8_geometry(K8Fwd& a) {
   a.by_tpt = k8_div_of(a.tpt);
   a.by_gdiv = k8_div_of(a.gdiv);
   a.whole_units = a.unit_rows == 64;
+  // of a unit, what it costs beside its chunks, in chunks; the most chunks that are not worth cutting
+  a.over = lat ? 0 : 1;
+  a.keep = lat ? 0 : 4;
 }
 
 size_t k8_fwd_workspace(K8Fwd a) {

@@ -31,6 +31,8 @@ __global__ void page_plan_kernel(PagePlan p) {
   int* pg = sm + p.B + 1;      // [B + 1]
   __shared__ long long wtok[32], wpage[32];
   __shared__ int fail;
+  pdl_trigger();
+  pdl_wait();
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int n_free = min(max(__ldg(p.n_free), 0), p.free_cap);
   if (tid == 0) fail = p.B;
@@ -120,9 +122,8 @@ cudaError_t launch_page_plan(const PagePlan& p, cudaStream_t st) {
   cudaError_t e = allow_smem(page_plan_kernel, (kPlanMaxBatch + 1) * 2 * (int)sizeof(int), done);
   if (e != cudaSuccess) return e;
   const int grid = min(148, max(1, (int)((p.T + (long long)block - 1) / block)));
-  page_plan_kernel<<<grid, block, smem, st>>>(p);
   count_launch();
-  return cudaGetLastError();
+  return launch_pdl(page_plan_kernel, (unsigned)grid, block, smem, st, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -289,6 +290,8 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 6) kv8_write_runs_kernel(c
   __shared__ int sums[NT / 32];
   __shared__ int found[4];  // first token, rows, page of the sequence, offset
   __shared__ const int* found_table;
+  pdl_trigger();
+  pdl_wait();
   const K8Cache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y, half = blockIdx.z;
   const int per = (c.B + NT - 1) / NT, b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
@@ -348,6 +351,8 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 6) kv8_write_runs_kernel(c
 template <bool F16, int NT, bool SHARED>
 __global__ void __launch_bounds__(SHARED ? NT : 2 * NT, 8) kv8_write_kernel(const __grid_constant__ K8Write a) {
   __shared__ float red[2][NT / 32];
+  pdl_trigger();
+  pdl_wait();
   const K8Cache& c = a.c;
   const int h = blockIdx.y, half = SHARED ? 0 : threadIdx.x / NT, tid = SHARED ? threadIdx.x : threadIdx.x % NT;
   int t = blockIdx.x * a.window;
@@ -390,26 +395,17 @@ cudaError_t launch_kv8_write(K8Write a, cudaStream_t st) {
   // window by window
   if (c.T >= 8ll * c.B) {
     const dim3 grid((unsigned)(c.T / c.ps + 2 * c.B), (unsigned)c.Hkv, c.shared ? 1 : 2);
-    if (c.dqk > 192) {
-      if (a.f16) kv8_write_runs_kernel<true, 512><<<grid, 512, 0, st>>>(a);
-      else kv8_write_runs_kernel<false, 512><<<grid, 512, 0, st>>>(a);
-    } else {
-      if (a.f16) kv8_write_runs_kernel<true, 128><<<grid, 128, 0, st>>>(a);
-      else kv8_write_runs_kernel<false, 128><<<grid, 128, 0, st>>>(a);
-    }
-  } else {
-    a.window = (int)max(1ll, (long long)c.T * c.Hkv / (148 * 16));
-    const dim3 grid((unsigned)((c.T + a.window - 1) / a.window), (unsigned)c.Hkv);
-    if (c.shared) {
-      if (a.f16) kv8_write_kernel<true, 64, true><<<grid, 64, 0, st>>>(a);
-      else kv8_write_kernel<false, 64, true><<<grid, 64, 0, st>>>(a);
-    } else {
-      if (a.f16) kv8_write_kernel<true, 32, false><<<grid, 64, 0, st>>>(a);
-      else kv8_write_kernel<false, 32, false><<<grid, 64, 0, st>>>(a);
-    }
+    const auto k = c.dqk > 192 ? (a.f16 ? kv8_write_runs_kernel<true, 512> : kv8_write_runs_kernel<false, 512>)
+                               : (a.f16 ? kv8_write_runs_kernel<true, 128> : kv8_write_runs_kernel<false, 128>);
+    count_launch();
+    return launch_pdl(k, grid, c.dqk > 192 ? 512u : 128u, 0, st, a);
   }
+  a.window = (int)max(1ll, (long long)c.T * c.Hkv / (148 * 16));
+  const dim3 grid((unsigned)((c.T + a.window - 1) / a.window), (unsigned)c.Hkv);
+  const auto k = c.shared ? (a.f16 ? kv8_write_kernel<true, 64, true> : kv8_write_kernel<false, 64, true>)
+                          : (a.f16 ? kv8_write_kernel<true, 32, false> : kv8_write_kernel<false, 32, false>);
   count_launch();
-  return cudaGetLastError();
+  return launch_pdl(k, grid, 64u, 0, st, a);
 }
 
 }  // namespace sa
