@@ -415,7 +415,7 @@ typedef struct sa_kv8_cache {
   int32_t n_heads_kv;      /* Hkv */
   int32_t d_qk, d_v;       /* 64/64, 128/128, 192/128; kv_shared: 128/128, 576/512 */
   int32_t kv_shared;       /* 1: V is the first d_v columns of k; v and v_scale are unused */
-  int32_t page_size;       /* rows per page */
+  int32_t page_size;       /* rows per page; page_size * n_pages < 2^31, page_size * max_pages <= 2^30 */
   int32_t n_pages;         /* pages in the cache */
   int32_t batch;           /* B sequences */
   int32_t max_pages;       /* pages per sequence in block_table */

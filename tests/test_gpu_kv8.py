@@ -141,6 +141,10 @@ CASES = {
                       fmt="int8", page=16, sinks=True),
     "latent_all": dict(lens=[333, 64, 129], new=[1, 3, 1], G=64, H=1, dqk=576, dv=512, shared=True),
     "latent_24": dict(lens=[100, 41], new=[1, 1], G=24, H=2, dqk=576, dv=512, shared=True, window=50),
+    "latent_64_int8": dict(lens=[700, 300, 20], new=[1, 1, 2], G=64, H=2, dqk=576, dv=512, shared=True, block=1, topk=200,
+                           fmt="int8", sinks=True),
+    "latent_50": dict(lens=[400, 129, 1], new=[1, 2, 1], G=50, H=1, dqk=576, dv=512, shared=True, dtype="fp16",
+                      window=200),
     "shared_128": dict(lens=[500, 33, 8], new=[2, 1, 8], G=32, H=1, dqk=128, dv=128, shared=True, dtype="fp16"),
     "shared_128_blocks": dict(lens=[500, 33], new=[2, 1], G=6, H=2, dqk=128, dv=128, shared=True, block=16, topk=6),
 }
@@ -173,6 +177,49 @@ def test_attend(name):
     torch.cuda.synchronize()
     assert cache.read_status() == L.SA_OK
     check(name, o, lse, ref, q.dtype, c["dqk"], max(c["lens"]))
+
+
+def test_many_requests_share_the_ctas():
+    """More units than CTAs, of every length: whole ones, cut ones, several in a CTA."""
+    rng = np.random.default_rng(51)
+    lens = np.concatenate([rng.integers(1, 60, 150), rng.integers(300, 900, 40), [4000, 0, 128, 129, 2500]]).tolist()
+    rng.shuffle(lens)
+    H, G, d, page = 3, 5, 64, 16
+    cache, table, kf, vf = make_cache(rng, lens, page=page, H=H, dqk=d, dv=d)
+    cu = np.arange(len(lens) + 1)
+    q = torch.randn((len(lens), H * G, d), device="cuda").to(torch.bfloat16)
+    o, lse = cache.attend(q, _i32(table), _i32(lens), cu_seqlens_q=_i32(cu))
+    ref = R.attend(q.double().cpu().numpy(), kf, vf, table, lens, cu, page, d ** -0.5)
+    check("many", o, lse, ref, q.dtype, d, 4000)
+
+
+@pytest.mark.parametrize("topk", [40, 300])
+def test_many_latent_tokens_share_the_ctas(topk):
+    rng = np.random.default_rng(52)
+    lens, new = [400, 35, 700], [60, 35, 20]
+    cache, table, kf, vf = make_cache(rng, lens, page=64, H=1, dqk=576, dv=512, shared=True)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    idx = make_idx(rng, lens, new, 1, 1, topk)
+    q = torch.randn((cu[-1], 128, 576), device="cuda").to(torch.bfloat16)
+    o, lse = cache.attend(q, _i32(table), _i32(lens), cu_seqlens_q=_i32(cu), idx=_i32(idx))
+    ref = R.attend(q.double().cpu().numpy(), kf, vf, table, lens, cu, 64, 576 ** -0.5, idx=idx)
+    check("latent many", o, lse, ref, q.dtype, 576, 700)
+
+
+def test_latent_codes_that_begin_between_32_bytes():
+    """A cache 16 bytes into its buffer: the kernel that reads 32 at a time cannot take it."""
+    rng = np.random.default_rng(53)
+    lens, cu = [150, 40], [0, 1, 2]
+    cache, table, kf, vf = make_cache(rng, lens, page=16, H=1, dqk=576, dv=512, shared=True)
+    buf = torch.empty(cache.k.numel() + 16, dtype=torch.uint8, device="cuda")
+    k = buf[16:].view(cache.k.dtype).view(cache.k.shape)
+    k.view(torch.uint8).copy_(cache.k.view(torch.uint8))
+    assert k.data_ptr() % 32 == 16
+    q = torch.randn((2, 64, 576), device="cuda").to(torch.bfloat16)
+    moved = Kv8Cache(k, None, cache.k_scale, None, d_v=512)
+    o, lse = moved.attend(q, _i32(table), _i32(lens), cu_seqlens_q=_i32(cu))
+    ref = R.attend(q.double().cpu().numpy(), kf, vf, table, lens, cu, 16, 576 ** -0.5)
+    check("moved", o, lse, ref, q.dtype, 576, 150)
 
 
 def test_attend_bsnd_strided_inputs_and_given_outputs():

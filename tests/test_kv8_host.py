@@ -99,6 +99,7 @@ BAD_CACHE = [
     (dict(n_pages=0), L.SA_ERR_PARAM), (dict(max_pages=0), L.SA_ERR_PARAM), (dict(table_stride=3), L.SA_ERR_PARAM),
     (dict(page_size=1 << 16, n_pages=1 << 15), L.SA_ERR_PARAM), (dict(batch=-1), L.SA_ERR_PARAM),
     (dict(page_size=1 << 20, max_pages=1 << 11, table_stride=1 << 11), L.SA_ERR_PARAM),
+    (dict(page_size=1 << 10, max_pages=(1 << 20) + 1, table_stride=1 << 21), L.SA_ERR_PARAM),
     (dict(t_q=-1), L.SA_ERR_PARAM), (dict(layout=0, s_q=1 << 30), L.SA_ERR_PARAM), (dict(k=None), L.SA_ERR_NULLPTR),
     (dict(v=None), L.SA_ERR_NULLPTR), (dict(v_scale=None), L.SA_ERR_NULLPTR), (dict(seq_lens=None), L.SA_ERR_NULLPTR),
     (dict(cu_seqlens_q=None), L.SA_ERR_NULLPTR), (dict(block_table=None), L.SA_ERR_NULLPTR),

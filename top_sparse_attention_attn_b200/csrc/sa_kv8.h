@@ -59,7 +59,7 @@ struct K8Fwd {
   int over, keep;   // see k8_begin
   int whole_units;  // rather a CTA per unit than parts, where that is nearly as even
   K8Div by_tpt, by_gdiv;
-  int win;           // rows before the token's own that it sees (INT_MAX: all)
+  int win;           // rows before the token's own that it sees (2^30: all)
   float scale_log2;  // scale * log2(e)
   const void* q;
   long long qstride;

@@ -2,7 +2,6 @@
 // held in 8 bits (sa_page_plan, sa_kv8_write, sa_kv8_fwd): host-side argument
 // validation and launches.
 #include <cuda_runtime.h>
-#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -27,9 +26,9 @@ sa_status validate_cache(const sa_kv8_cache* c) {
   if (c->d_qk < 16 || c->d_v < 16 || c->d_qk % 16 || c->d_v % 16 || c->d_qk > 576 || c->d_v > 512) return SA_ERR_PARAM;
   if (c->kv_shared && c->d_v > c->d_qk) return SA_ERR_PARAM;
   if (c->page_size < 1 || c->n_pages < 1 || c->max_pages < 1 || c->batch < 0) return SA_ERR_PARAM;
-  // rows are numbered in 32 bits, inside the cache and inside a sequence
+  // rows are numbered in 32 bits: inside the cache, and with room to spare inside a sequence
   if ((long long)c->page_size * c->n_pages >= (1ll << 31)) return SA_ERR_PARAM;
-  if ((long long)c->page_size * c->max_pages >= (1ll << 31)) return SA_ERR_PARAM;
+  if ((long long)c->page_size * c->max_pages > (1ll << 30)) return SA_ERR_PARAM;
   if (c->table_stride < c->max_pages) return SA_ERR_PARAM;
   if (c->layout == SA_LAYOUT_BSND ? c->s_q < 0 : c->t_q < 0) return SA_ERR_PARAM;
   const long long T = tokens_of(c);
@@ -99,7 +98,7 @@ sa::K8Fwd make_fwd(const sa_kv8_cache* c, const sa_kv8_query* q) {
   r.bs = q->block_size;
   r.by_bs = sa::k8_div_of(q->block_size);
   r.topk = q->topk;
-  r.win = q->win_left < 0 || q->win_left > INT_MAX ? INT_MAX : (int)q->win_left;
+  r.win = q->win_left < 0 || q->win_left > (1 << 30) ? 1 << 30 : (int)q->win_left;  // no sequence is longer
   r.scale_log2 = q->scale * 1.4426950408889634f;
   r.q = q->q;
   r.qstride = q->q_stride;
@@ -120,7 +119,7 @@ sa_status sa_page_plan(const sa_page_plan_args* a, void* stream) {
   if (a->batch < 0 || a->batch > sa::kPlanMaxBatch || a->max_pages < 1 || a->page_size < 1 || a->n_tokens < 0 ||
       a->free_capacity < 0 || a->table_stride < a->max_pages)
     return SA_ERR_PARAM;
-  if ((long long)a->max_pages * a->page_size >= (1ll << 31)) return SA_ERR_PARAM;
+  if ((long long)a->max_pages * a->page_size > (1ll << 30)) return SA_ERR_PARAM;
   if (a->batch > 0 && (!a->old_lens || !a->new_lens || !a->block_table || !a->seq_lens)) return SA_ERR_NULLPTR;
   if (!a->n_free || !a->cu_seqlens_q || !a->n_free_out || !a->n_served) return SA_ERR_NULLPTR;
   if ((a->n_tokens > 0 && !a->slots) || (a->free_capacity > 0 && !a->free_pages)) return SA_ERR_NULLPTR;

@@ -1061,15 +1061,14 @@ static cudaError_t split_d(const K8Fwd& a, void* ws, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 // a shared row of 576 columns, V its first 512
 // ---------------------------------------------------------------------------
-// A unit is one token and 16 MT of its heads (MT = 4 where there are more than 32); 64
-// rows per chunk and one CTA of 8 warps per SM, on the same line of chunks as above.  The
-// rows, selected one by one, are copied whole (cp.async, three stages), and serve as K and
-// V.  For the scores warp (mg, tg) takes the row tiles of its half of the heads against 16
-// of the rows (MT = 4), so that each code is converted twice; for O a warp takes all
-// heads against 64 of the columns.  P goes through shared memory between the two.  The
-// running maximum is shared by the CTA and looked at with the barrier that the stages
-// need anyway; it is exchanged only when some row's grew by more than 2^kK8Grow.
-// Bound: m16n8k16 issues (1024 products per cycle and SM), 64 rows x 64 heads in 4352 cycles.
+// Up to 32 heads (more: the next section).  A unit is one token and 16 MT of its heads, MT = 1
+// or 2; 64 rows per chunk and one CTA of 8 warps per SM, on the same line of chunks as
+// above.  The rows, selected one by one, are copied whole (cp.async, three stages), and serve
+// as K and V.  For the scores warp (mg, tg) takes 16 of the heads against its share of the rows;
+// for O a warp takes all heads against 64 of the columns.  P goes through shared memory
+// between the two.  The running maximum is shared by the CTA and looked at with the
+// barrier that the stages need anyway; it is exchanged only when some row's grew by more
+// than 2^kK8Grow.
 constexpr int kLatRows = 64, kLatDK = 576, kLatDV = 512;
 
 template <int MT>
@@ -1084,7 +1083,7 @@ struct K8Lat {
   static constexpr int kMeta = kLatRows * 8;  // row, scale
   static constexpr int kRedAt = kMetaAt + kStages * kMeta;
   static constexpr int kSmem = kRedAt + 8 * MT * 16 * 4 + MT * 16 * 8;
-  // scores: warps along the heads and along the rows
+  // scores: warps along the heads and along the rows, row tiles of heads and of rows of a warp
   static constexpr int kMG = MT == 1 ? 1 : 2, kTG = 8 / kMG, kMT = MT / kMG, kNT = kLatRows / 8 / kTG;
 };
 // piece p of row r (rows of 36 pieces, 64 bytes out of step with 128): 8 rows' same piece,
@@ -1105,6 +1104,7 @@ __global__ void __launch_bounds__(256, 1) k8_latent_kernel(const __grid_constant
   uint32_t* const sq = reinterpret_cast<uint32_t*>(smem + P::kQAt);
   const uint32_t sp_at = smem_u32(smem + P::kPAt);
   pdl_trigger();
+  pdl_wait();
   K8Cursor cur;
   if (!k8_begin<256>(a, ws, tid, found, cur)) return;
   const int krs = c.Hkv * kLatDK;
@@ -1933,9 +1933,8 @@ static cudaError_t latent_t(const K8Fwd& a, void* ws, cudaStream_t st) {
   cudaError_t e = allow_smem(k, P::kSmem, done);
   if (e != cudaSuccess) return e;
   const int n = k8_ctas(a);
-  k<<<(unsigned)n, 256, P::kSmem, st>>>(a, static_cast<float*>(ws));
   count_launch();
-  e = cudaGetLastError();
+  e = launch_pdl(k, (unsigned)n, 256, P::kSmem, st, a, static_cast<float*>(ws));
   if (e != cudaSuccess || n == 1) return e;
   count_launch();
   return launch_pdl(k8_join_kernel<MT * 16, kLatDV>, (unsigned)n, 256, 0, st, a, static_cast<float*>(ws), n);
