@@ -610,6 +610,37 @@ def test_serving_steps(fmt, shared):
     assert cache.read_status() == L.SA_OK
 
 
+def test_given_stream():
+    """A call on a stream that is not the current one: its workspace belongs to that stream."""
+    rng = np.random.default_rng(42)
+    lens, cu = [3000, 129], [0, 1, 2]
+    cache, table, kf, vf = make_cache(rng, lens, page=64, H=2, dqk=128, dv=128)
+    q = torch.randn((2, 16, 128), device="cuda").to(torch.bfloat16)
+    tab, ln, cu_d = _i32(table), _i32(lens), _i32(cu)
+    ref = R.attend(q.double().cpu().numpy(), kf, vf, table, lens, cu, 64, 128 ** -0.5)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for raw in (side.cuda_stream, 0):
+        outs = []
+        for _ in range(10):
+            outs.append(cache.attend(q, tab, ln, cu_seqlens_q=cu_d, stream=raw))
+            torch.full((4 << 20,), 7, dtype=torch.int32, device="cuda")   # takes freed memory of the current stream
+        torch.cuda.synchronize()
+        for o, lse in outs:
+            check("stream", o, lse, ref, q.dtype, 128, 3000)
+    p = plan_pages(_i32([0, 5]), _i32([3, 1]), _i32([[-1], [4]]), _i32([1, 2]), _i32([2]), page_size=16, n_tokens=4,
+                   stream=side.cuda_stream)
+    side.synchronize()
+    assert p.slots.tolist() == [32, 33, 34, 69] and int(p.n_free) == 1
+    k = torch.randn((2, 2, 128), device="cuda").to(torch.bfloat16)
+    torch.cuda.synchronize()
+    cache.write(k, k, tab, ln, cu_seqlens_q=cu_d, stream=side.cuda_stream)
+    side.synchronize()
+    got = cache.k[int(table[1, 2]), 0].float() * cache.k_scale[int(table[1, 2])][:, None]
+    assert (got - k[1].float()).abs().max() <= k[1].float().abs().max() / 16
+    assert cache.read_status() == L.SA_OK
+
+
 def test_graph_replay_and_two_streams():
     """A step captured and replayed with new contents in the same buffers; two steps on two
     streams at once, a workspace each."""

@@ -132,11 +132,28 @@ int64_t integer(PyObject* o, const char* name) {
   return v;
 }
 
-void* stream_of(PyObject* o, int index) {
-  if (index < 0) value_error("the tensors are on the CPU: a CUDA device expected");
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream();
-  return reinterpret_cast<void*>((uintptr_t)integer(o, "stream"));
-}
+// Makes the device and the call's stream (a cudaStream_t as an integer, None for the current
+// one) current, so that what the call allocates belongs to that stream.
+class OnStream {
+ public:
+  OnStream(PyObject* o, int index) {
+    if (index < 0) value_error("the tensors are on the CPU: a CUDA device expected");
+    if (o == Py_None) {
+      device_.set_index((c10::DeviceIndex)index);
+    } else {
+      const auto raw = reinterpret_cast<cudaStream_t>((uintptr_t)integer(o, "stream"));
+      stream_.reset_stream(raw ? c10::cuda::getStreamFromExternal(raw, (c10::DeviceIndex)index)
+                               : c10::cuda::getDefaultCUDAStream((c10::DeviceIndex)index));
+    }
+    raw_ = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream();
+  }
+  void* get() const { return raw_; }
+
+ private:
+  c10::cuda::OptionalCUDAGuard device_;
+  c10::cuda::OptionalCUDAStreamGuard stream_;
+  void* raw_ = nullptr;
+};
 
 // The cache (a bytes object that holds its sa_kv8_cache, and its device index) with a
 // step's tokens in it.
@@ -199,7 +216,7 @@ PyObject* kv8_plan(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
   a.n_free = need_i32(v[4], "n_free", index, 1);
   a.page_size = to_i32(integer(v[5], "page_size"), "page_size");
   a.n_tokens = to_i32(integer(v[6], "n_tokens"), "n_tokens");
-  void* st = stream_of(v[7], index);
+  const OnStream st(v[7], index);
   // one allocation: slots, then the int32 outputs
   const int64_t T = a.n_tokens > 0 ? a.n_tokens : 0;
   const at::Tensor all = at::empty({T + B + 2}, old.options().dtype(at::kLong));
@@ -211,8 +228,7 @@ PyObject* kv8_plan(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
   a.n_free_out = static_cast<int32_t*>(left.data_ptr());
   a.n_served = static_cast<int32_t*>(served.data_ptr());
   a.slots = static_cast<int64_t*>(slots.data_ptr());
-  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
-  const sa_status status = sa_page_plan(&a, st);
+  const sa_status status = sa_page_plan(&a, st.get());
   if (status != SA_OK) return PyLong_FromLong(status);
   PyObject* r = PyTuple_New(5);
   if (!r) return nullptr;
@@ -240,9 +256,8 @@ PyObject* kv8_write(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     r.v_stride = token_step(x, "v", c.n_heads_kv, c.d_v, index);
     r.v = x.data_ptr();
   }
-  void* st = stream_of(v[7], index);
-  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
-  return PyLong_FromLong(sa_kv8_write(&c, &r, st));
+  const OnStream st(v[7], index);
+  return PyLong_FromLong(sa_kv8_write(&c, &r, st.get()));
   KV8_END
 }
 
@@ -291,7 +306,7 @@ PyObject* kv8_attend(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
   const c10::IntArrayRef o_shape(shape), lse_shape = o_shape.slice(0, n - 1);
   if (v[12] != Py_None) a.o = need(v[12], "o", q.scalar_type(), index, o_shape);
   if (v[13] != Py_None) a.lse = static_cast<float*>(need(v[13], "lse", at::kFloat, index, lse_shape));
-  void* st = stream_of(v[14], index);
+  const OnStream st(v[14], index);
   at::Tensor o, lse;
   if (v[12] == Py_None) {
     o = at::empty(o_shape, q.options());
@@ -304,9 +319,8 @@ PyObject* kv8_attend(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
   size_t bytes = 0;
   sa_status status = sa_kv8_fwd_get_workspace_size(&c, &a, &bytes);
   if (status != SA_OK) return PyLong_FromLong(status);
-  const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
   const c10::DataPtr ws = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
-  status = sa_kv8_fwd(&c, &a, ws.get(), bytes, st);
+  status = sa_kv8_fwd(&c, &a, ws.get(), bytes, st.get());
   if (status != SA_OK) return PyLong_FromLong(status);
   PyObject* r = PyTuple_New(2);
   if (!r) return nullptr;
