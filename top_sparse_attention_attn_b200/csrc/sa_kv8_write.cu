@@ -163,6 +163,18 @@ __device__ __forceinline__ void k8_unpack8(const uint4& r, float (&x)[8]) {
   }
 }
 
+// Of two pairs of 16-bit floats, the larger magnitudes (a magnitude of NaN is passed over).
+template <bool F16>
+__device__ __forceinline__ uint32_t k8_absmax2(uint32_t a, uint32_t b) {
+  b &= 0x7fff7fffu;
+  if (F16) {
+    const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
 // m new rows (x, `stride` apart) of head h to rows [off, off + m) of the page that `table`
 // names, none if it names none of the cache; NT threads, which meet at named barrier `bar`.
 // The rows are fetched before the table's answer is looked at.  A thread keeps its first kHold pieces of 8 elements
@@ -195,31 +207,53 @@ __device__ __forceinline__ void k8_write_part(const char* x, long long stride, i
   const long long row_bytes = (long long)cc.Hkv * d;
   uint8_t* const codes = cache + (long long)page * cc.ps * row_bytes + (long long)h * d;
   const float before = off ? *scale : 0.f;
+  // The maximum, two elements at a time (NaN loses); once more, one by one, where it is infinite: infinities
+  // and NaN set no scale.
   float a = 0.f;
-  auto most = [&](const uint4& w) {
-    float v[8];
-    k8_unpack8<F16>(w, v);
+  auto reduce = [&](auto&& most) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float s = fabsf(v[j]);
-      a = fmaxf(a, s < INFINITY ? s : 0.f);  // infinities and NaN set no scale
+    for (int j = 0; j < kHold; ++j)
+      if (tid + j * NT < n8) most(hold[j]);
+    for (int i = tid + kHold * NT; i < n8; i += NT) {
+      int r, c;
+      piece(i, r, c);
+      most(__ldg(reinterpret_cast<const uint4*>(x + r * stride * 2 + c * 16)));
     }
   };
+  auto meet = [&]() {
 #pragma unroll
-  for (int j = 0; j < kHold; ++j)
-    if (tid + j * NT < n8) most(hold[j]);
-  for (int i = tid + kHold * NT; i < n8; i += NT) {
-    int r, c;
-    piece(i, r, c);
-    most(__ldg(reinterpret_cast<const uint4*>(x + r * stride * 2 + c * 16)));
+    for (int s = 16; s; s >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, s));
+    if ((tid & 31) == 0) red[tid >> 5] = a;
+    asm volatile("bar.sync %0, %1;\n" ::"r"(bar), "n"(NT) : "memory");
+    a = red[0];
+#pragma unroll
+    for (int w = 1; w < NT / 32; ++w) a = fmaxf(a, red[w]);
+  };
+  uint32_t two = 0;
+  reduce([&](const uint4& w) {
+    two = k8_absmax2<F16>(two, w.x);
+    two = k8_absmax2<F16>(two, w.y);
+    two = k8_absmax2<F16>(two, w.z);
+    two = k8_absmax2<F16>(two, w.w);
+  });
+  const float2 halves = F16 ? __half22float2(*reinterpret_cast<const __half2*>(&two))
+                            : make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+  a = fmaxf(halves.x, halves.y);
+  meet();
+  if (!(a < INFINITY)) {
+    asm volatile("bar.sync %0, %1;\n" ::"r"(bar), "n"(NT) : "memory");  // red has been read
+    a = 0.f;
+    reduce([&](const uint4& w) {
+      float v[8];
+      k8_unpack8<F16>(w, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float s = fabsf(v[j]);
+        a = fmaxf(a, s < INFINITY ? s : 0.f);
+      }
+    });
+    meet();
   }
-#pragma unroll
-  for (int s = 16; s; s >>= 1) a = fmaxf(a, __shfl_xor_sync(~0u, a, s));
-  if ((tid & 31) == 0) red[tid >> 5] = a;
-  asm volatile("bar.sync %0, %1;\n" ::"r"(bar), "n"(NT) : "memory");
-  a = red[0];
-#pragma unroll
-  for (int w = 1; w < NT / 32; ++w) a = fmaxf(a, red[w]);
   int e = k8_exp_for(a, fmt);
   if (off) e = max(e, k8_exp_at_least(before));
   const float after = k8_pow2(e), inv = k8_pow2(-e);  // x * 2^-e is x / s exactly
