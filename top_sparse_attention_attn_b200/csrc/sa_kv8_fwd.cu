@@ -939,7 +939,8 @@ __global__ void __launch_bounds__(256) k8_join_kernel(const K8Fwd a, float* ws, 
   constexpr int NV = DV < 128 ? 1 : DV / 128, kLanes = DV < 128 ? DV / 4 : 32;  // float4 of a lane, lanes
   __shared__ float sl[8];
   __shared__ float4 so[8][NV * kLanes];
-  pdl_trigger();
+  // No early launch of what comes behind: another attention's CTAs, placed while these still run, end up
+  // unevenly on the SMs (387 instead of 255 us a call, one long decode step behind the other).
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll 1
