@@ -145,6 +145,16 @@ CASES = {
                            fmt="int8", sinks=True),
     "latent_50": dict(lens=[400, 129, 1], new=[1, 2, 1], G=50, H=1, dqk=576, dv=512, shared=True, dtype="fp16",
                       window=200),
+    # tokens enough for the tensor-memory kernel
+    "latents_rows": dict(lens=[600, 70, 1, 0, 333], new=[9, 7, 1, 1, 8], G=128, H=1, dqk=576, dv=512, shared=True, block=1,
+                         topk=130),
+    "latents_all": dict(lens=[333, 64, 129], new=[10, 6, 9], G=64, H=1, dqk=576, dv=512, shared=True, power=False),
+    "latents_64_int8": dict(lens=[700, 300, 20], new=[4, 5, 9], G=64, H=2, dqk=576, dv=512, shared=True, block=1,
+                            topk=200, fmt="int8", sinks=True),
+    "latents_50": dict(lens=[400, 129, 1], new=[9, 12, 1], G=50, H=1, dqk=576, dv=512, shared=True, dtype="fp16",
+                       window=200),
+    "latents_blocks": dict(lens=[500, 77], new=[14, 14], G=33, H=1, dqk=576, dv=512, shared=True, block=16, topk=13,
+                           page=16, fmt="int8"),
     "shared_128": dict(lens=[500, 33, 8], new=[2, 1, 8], G=32, H=1, dqk=128, dv=128, shared=True, dtype="fp16"),
     "shared_128_blocks": dict(lens=[500, 33], new=[2, 1], G=6, H=2, dqk=128, dv=128, shared=True, block=16, topk=6),
 }
@@ -257,7 +267,8 @@ def test_rows_behind_the_last_sequence_stay(topk):
     assert (o[3:] == 7).all() and (lse[3:] == 7).all() and cache.read_status() == L.SA_OK
 
 
-@pytest.mark.parametrize("name", ["chunk", "window", "blocks", "latent_rows", "page7"])
+@pytest.mark.parametrize("name", ["chunk", "window", "blocks", "latent_rows", "latents_rows", "latents_all",
+                                  "page7"])
 def test_rows_that_are_not_seen_may_hold_anything(name):
     """NaN codes and scales of rows behind a token (or before its window) leave it alone."""
     c, cache, table, kf, vf, q, idx, sinks, cu = _problem(name)

@@ -1259,6 +1259,7 @@ __global__ void __launch_bounds__(256, 1) k8_latent_kernel(const __grid_constant
       const float* fm = reinterpret_cast<const float*>(im) + 64;
       fill = at;
       at = at + 1 == S ? 0 : at + 1;
+      if (!__any_sync(~0u, im[lane] >= 0 || im[lane + 32] >= 0)) continue;  // no row in it, as all warps see
 
       // --- scores ---
       float s[P::kMT][P::kNT][4];
@@ -1957,8 +1958,14 @@ static cudaError_t latent_f(const K8Fwd& a, void* ws, cudaStream_t st) {
 
 static void k8_geometry(K8Fwd& a) {
   const bool lat = k8_latent(a);
-  // (the tcgen05 kernel reads codes 32 bytes at a time)
-  a.unit_rows = !lat ? 16 : a.G <= 16 ? 16 : a.G <= 32 || ((uintptr_t)a.c.k & 31) ? 32 : 64;
+  // More than 32 heads of a shared row go to the tcgen05 kernel (64 heads x 128 rows a step; it reads codes
+  // 32 bytes at a time), but not where shares of 32 heads x 64 rows leave SMs idle: its start and end cost
+  // 13 us more.  There mma.sync took 16.5 us against 29 (a token, 2048 rows, 128 heads), 11.7 against 20.5
+  // (4 tokens, 36 rows); beyond, 142 against 105 (48 tokens, 2048 rows), 30 against 26.4 (8 tokens, 1024).
+  const long long small = (long long)a.c.T * a.c.Hkv * ((a.G + 31) / 32) *
+                          (a.topk ? ((long long)a.topk * a.bs + 63) / 64 : ((long long)a.c.max_pages * a.c.ps + 63) / 64);
+  const bool tc = a.G > 32 && small > 148 && ((uintptr_t)a.c.k & 31) == 0;
+  a.unit_rows = !lat || a.G <= 16 ? 16 : tc ? 64 : 32;
   a.chunk = !lat ? kK8Chunk : a.unit_rows == 64 ? kTcRows : kLatRows;
   a.gdiv = min(a.G, a.unit_rows);
   a.hs = (a.G + a.unit_rows - 1) / a.unit_rows;
