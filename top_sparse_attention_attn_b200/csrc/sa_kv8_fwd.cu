@@ -296,10 +296,7 @@ __device__ __forceinline__ bool k8_begin(const K8Fwd& a, float* ws, int tid, K8F
     if (x < warp) at += f.sum[x];
   }
   int n_cta = (int)min(W, (long long)gridDim.x);  // a share is empty only in CTAs behind these
-  // Units of one length, and nearly as many as CTAs: one each.  Cutting them evenly would
-  // leave parts to join (131 KB each of 64 heads x 512), which costs as much as 5 chunks.
-  if (a.whole_units && a.sel_ch && W <= (long long)gridDim.x * a.sel_ch && 5 * W >= 3ll * gridDim.x * a.sel_ch)
-    n_cta = (int)(W / a.sel_ch);
+  if (a.whole_units) n_cta = (int)min(W / a.sel_ch, (long long)n_cta);  // a CTA each
   if (tid < 2) (reinterpret_cast<K8Join*>(ws) + 2 * blockIdx.x)[tid].n = 0;
   if (blockIdx.x >= n_cta) return false;
   if (W <= 0x7fffffff) {
@@ -1016,6 +1013,7 @@ static bool k8_latent(const K8Fwd& a) { return a.c.dqk > 192; }
 
 // CTAs: all that the SMs hold at once, or as many as the longest possible line has chunks.
 static int k8_ctas(const K8Fwd& a) {
+  if (a.whole_units) return a.c.T * a.hs * a.c.Hkv;
   const int occ = k8_latent(a) ? 1 : a.c.dqk + a.c.dv <= 128 ? 4 : (a.c.dqk <= 128 ? 3 : 2);
   const long long units = ((long long)(a.c.T + a.tpt - 1) / a.tpt + (a.tpt > 1 ? min(a.c.B, a.c.T) : 0)) * a.hs * a.c.Hkv;
   long long ch = a.sel_ch;
@@ -1484,7 +1482,7 @@ struct K8Tc {
   static constexpr int kMetaAt = kQAt + 9 * 64 * 128;       // [2][128] rows seen, [2][128] scales
   static constexpr int kHeadAt = kMetaAt + 2 * kTcRows * 8;  // [64] (fr, base)
   static constexpr int kRedAt = kHeadAt + 64 * 8;            // [4][64]
-  static constexpr int kBarAt = kRedAt + 4 * 64 * 4;         // full [4], p_full, s_done, free [4]
+  static constexpr int kBarAt = kRedAt + 4 * 64 * 4;         // full [2], p_full, s_done, free [4]
   static constexpr int kSmem = kBarAt + 16 * 8 + 1024;
   static constexpr uint32_t kTmemS = 256;  // column of S^T behind the four blocks of O^T
 };
@@ -1507,6 +1505,17 @@ __device__ __forceinline__ bool tc_any(bool x) {
 struct K8Codes {
   uint32_t w[8];
 };
+// hi: the upper half of both operands' descriptors; one thread of the warp issues (tc_elect)
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(hi), "r"(id), "r"(acc));
+}
+__device__ __forceinline__ bool tc_elect() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
+}
 __device__ __forceinline__ K8Codes tc_ld32(const uint8_t* p) {  // 32 codes, 32-byte aligned; none: zeros
   K8Codes r;
   if (p) {
@@ -1531,10 +1540,10 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
   const K8Cache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + P::kBarAt);
-  uint64_t *const p_full = full + 4, *const s_done = full + 5, *const blk_free = full + 6;
+  uint64_t *const p_full = full + 2, *const s_done = full + 3, *const blk_free = full + 4;
   if (tid == 0) {
-    for (int i = 0; i < 5; ++i) mbar_init(full + i, 8);
-    for (int i = 5; i < 10; ++i) mbar_init(full + i, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(full + i, 8);
+    for (int i = 3; i < 8; ++i) mbar_init(full + i, 1);
     mbar_fence_init();
     abort_word = 0;
   }
@@ -1556,38 +1565,44 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
     // --- the MMAs ---
-    if (warp == 8 && lane == 0 && some) {
+    if (warp == 8 && some) {
       const uint32_t kat = smem_u32(smem), qat = kat + P::kQAt, pat = kat + 8 * kTcSlab;
-      const uint64_t dk = sdesc(kat, 0, 1024), dq = sdesc(qat, 0, 1024);
-      const uint64_t dv = sdesc(kat, kTcSlab, 1024), dp = sdesc(pat, kTcSlab, 1024);
+      const uint32_t dk = (uint32_t)sdesc(kat, 0, 1024), dq = (uint32_t)sdesc(qat, 0, 1024);
+      const uint32_t dv = (uint32_t)sdesc(kat, kTcSlab, 1024), dp = (uint32_t)sdesc(pat, kTcSlab, 1024);
+      const uint32_t hi = (uint32_t)(sdesc(0, 0, 1024) >> 32);
       constexpr uint32_t id_s = k8_idesc(128, 64, false, false), id_o = k8_idesc(128, 64, true, true);
       for (long long n = 0; n < n_chunks; ++n) {
         const uint32_t ph = (uint32_t)(n & 1);
         bool ok = true;
-        // Unrolled with constant offsets: an addition carried from MMA to MMA took 120 to 170 cycles
-        // each.  The bases are hidden from the compiler, which would keep 100 sums of them otherwise.
-        uint64_t A = dk, B = dq, C = dv, D = dp;
-        asm volatile("" : "+l"(A), "+l"(B), "+l"(C), "+l"(D));
+        // Unrolled with constant offsets from bases that the compiler sees to be alike in the whole warp, so that
+        // a descriptor takes one addition in the warp's own registers; 32 bits of it, the others never change.
+        // (Additions carried from MMA to MMA took 120 to 170 cycles each, one thread's registers 8 % more.)
 #pragma unroll
         for (int sl = 0; sl < kTcSlabs; ++sl) {
-          if ((sl & 1) == 0 && sl < 8) {  // slabs in pairs, the ninth with the last
-            ok = ok && mbar_wait(full + (sl >> 1), ph, &abort_word, c.status);
+          if ((sl & 3) == 0 && sl < 8) {  // four slabs, then five: a wait and its fence cost 300 to 500 cycles
+            ok = ok && mbar_wait(full + (sl >> 2), ph, &abort_word, c.status);
+            fence_async_smem();
             tc_fence_after();
           }
+          if (tc_elect()) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            mma_bf16(tmem + P::kTmemS, desc_add(A, sl * kTcSlab + 32 * e), desc_add(B, sl * 8192 + 32 * e), id_s, sl || e);
+            tc_mma(tmem + P::kTmemS, dk + ((sl * kTcSlab + 32 * e) >> 4), dq + ((sl * 8192 + 32 * e) >> 4), hi, id_s, sl || e);
+          if (sl == kTcSlabs - 1) mma_commit(s_done);
+          }
         }
-        mma_commit(s_done);
         if (!ok || !mbar_wait(p_full, ph, &abort_word, c.status)) break;
+        fence_async_smem();
         tc_fence_after();
         const uint32_t over = *(volatile int*)&fresh;
 #pragma unroll
         for (int mb = 0; mb < 4; ++mb) {
+          if (tc_elect()) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            mma_bf16(tmem + mb * 64, desc_add(C, mb * 2 * kTcSlab + 2048 * e), desc_add(D, 2048 * e), id_o, !over || e);
+            tc_mma(tmem + mb * 64, dv + ((mb * 2 * kTcSlab + 2048 * e) >> 4), dp + ((2048 * e) >> 4), hi, id_o, !over || e);
           mma_commit(blk_free + mb);
+          }
         }
       }
       if (abort_word) mbar_wait_drain(blk_free + 3, 0);  // bounded: what was issued before the wait gave up
@@ -1629,18 +1644,26 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
         return row < u.hi && row >= u.lo ? row : -1;
       };
       auto fetch_page = [&](int row) -> int { return row >= 0 ? __ldg(u.table + k8_quot(c.by_ps, row)) : 0; };
-      // the lane's two rows of the codes and its row's scale, from what was looked up
-      const uint8_t* ptr[3];  // pairs of slabs: rows 8 j + lane / 4, 32 codes of 128; the ninth: row lane / 2
+      // the lane's row of the cache, from what was looked up (-1: none), and its scale
       float ks_next = 0.f;
-      bool see_next = false;
-      auto point = [&](int row, int page) {
+      auto place = [&](int row, int page) -> int {
         if (row >= 0 && (page < 0 || page >= c.n_pages)) {
           if (c.status) atomicOr(c.status, kStatusIndexRange);
           row = -1;
         }
-        const int rr = row >= 0 ? page * c.ps + k8_rem(c.by_ps, row) : -1;
-        see_next = row >= 0;
-        if (see_next) ks_next = __ldg(c.ks + (long long)page * c.Hkv + u.h);
+        if (row < 0) return -1;
+        ks_next = __ldg(c.ks + (long long)page * c.Hkv + u.h);
+        return page * c.ps + k8_rem(c.by_ps, row);
+      };
+      auto note = [&](uint32_t ph, int rr) {  // for the softmax
+        if (lane < 16) {
+          see_of[ph * kTcRows + warp * 16 + lane] = rr >= 0;
+          scale_of[ph * kTcRows + warp * 16 + lane] = ks_next;
+        }
+      };
+      // the lane's pieces of the codes.  Pairs of slabs: rows 8 j + lane / 4, 32 codes of 128; the ninth: row lane / 2
+      const uint8_t* ptr[3];
+      auto point = [&](int rr) {
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
           const int at = __shfl_sync(~0u, rr, j < 2 ? 8 * j + (lane >> 2) : lane >> 1);
@@ -1648,7 +1671,17 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
           ptr[j] = at >= 0 ? c.k + (long long)at * krs + u.h * kLatDK + col : nullptr;
         }
       };
-      int x0 = fetch_idx(0), x1 = fetch_idx(1), next_x = fetch_idx(2);
+      auto prefetch = [&](int rr) {  // 8 rows of 576 bytes: 4 lanes a row, 128 bytes apart, and the last 64
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int at = __shfl_sync(~0u, rr, 8 * j + (lane >> 2));
+          if (at < 0) continue;
+          const uint8_t* const p = c.k + (long long)at * krs + u.h * kLatDK + (lane & 3) * 128;
+          asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p));
+          if ((lane & 3) == 3) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p + 128));
+        }
+      };
+      int x0 = fetch_idx(0), x1 = fetch_idx(1), x2 = fetch_idx(2), next_x = fetch_idx(3);
       // --- Q, 8 lanes a row, as halves times 2^(14 - E); the scores of the unit before have been taken ---
       uint4 qr[2][9];
 #pragma unroll
@@ -1659,20 +1692,21 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
         for (int i = 0; i < 9; ++i)
           qr[y][i] = row < u.rows ? __ldg(reinterpret_cast<const uint4*>(src + ((lane & 7) + 8 * i) * 16)) : make_uint4(0, 0, 0, 0);
       }
-      const int row0 = resolve(0, x0), pg0 = fetch_page(row0);
-      int next_row = resolve(1, x1), next_page = fetch_page(next_row);
+      const int row0 = resolve(0, x0), pg0 = fetch_page(row0), row1 = resolve(1, x1), pg1 = fetch_page(row1);
+      int next_row = resolve(2, x2), next_page = fetch_page(next_row);
       K8Codes raw[9];  // pair g, row j: 2 g + j
-      auto load_a = [&]() {
+      auto load = [&](int g) {  // pair g of slabs, the ninth with the last
 #pragma unroll
-        for (int x = 0; x < 4; ++x) raw[x] = tc_ld32(ptr[x & 1] ? ptr[x & 1] + (x >> 1) * 128 : nullptr);
+        for (int j = 0; j < 2; ++j) raw[2 * g + j] = tc_ld32(ptr[j] ? ptr[j] + g * 128 : nullptr);
+        if (g == 3) raw[8] = tc_ld32(ptr[2]);
       };
-      auto load_b = [&]() {
+      int rr = place(row0, pg0);
+      point(rr);
 #pragma unroll
-        for (int x = 4; x < 8; ++x) raw[x] = tc_ld32(ptr[x & 1] ? ptr[x & 1] + (x >> 1) * 128 : nullptr);
-        raw[8] = tc_ld32(ptr[2]);
-      };
-      point(row0, pg0);
-      load_a(); load_b();
+      for (int g = 0; g < 4; ++g) load(g);
+      note((uint32_t)(n & 1), rr);
+      rr = place(row1, pg1);
+      prefetch(rr);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int row = 32 * y + warp * 4 + (lane >> 3), qp = lane & 7;
@@ -1711,21 +1745,8 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
       bool first = true;
       for (int k = 0; k < n_steps; ++k, ++n) {
         const uint32_t ph = (uint32_t)(n & 1);
-        // --- codes to halves, slab by slab ---
-        if (lane < 16) {
-          see_of[ph * kTcRows + warp * 16 + lane] = see_next;
-          scale_of[ph * kTcRows + warp * 16 + lane] = ks_next;
-        }
-        point(next_row, next_page);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)  // 8 rows of 576 bytes: 4 lanes a row, 128 bytes apart, and the last 64
-          if (ptr[j]) {
-            asm volatile("prefetch.global.L2 [%0];\n" ::"l"(ptr[j] + (lane & 3) * 96));  // 128 apart
-            if ((lane & 3) == 0) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(ptr[j] + 544));
-          }
-        next_row = resolve(k + 2, next_x);
-        next_page = fetch_page(next_row);
-        next_x = fetch_idx(k + 3);
+        // --- codes to halves, slab by slab; the next chunk's take their place ---
+        point(k + 1 < n_steps ? rr : -1);
         // 32 codes to 64 bytes of slab `sl`, row r, from its 16-byte piece ch0 on.  The order of the pieces
         // keeps eight lanes' stores (two rows, two slabs) on different banks.
         auto put = [&](const K8Codes& x, int sl, int r, int ch0, int turn) {
@@ -1746,11 +1767,22 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
           for (int j = 0; j < 2; ++j)
             put(raw[2 * g + j], 2 * g + ((lane >> 1) & 1), warp * 16 + 8 * j + (lane >> 2), 4 * (lane & 1), lane & 2);
           if (g == 3) put(raw[8], 8, warp * 16 + (lane >> 1), 4 * (lane & 1), 0);
-          fence_async_smem();  // costs some 300 cycles: once for a pair of slabs
-          __syncwarp();
-          if (lane == 0) mbar_arrive(full + g);
+          // (the thread that issues the MMAs has the fence between these stores and their reads; here it would
+          // wait for the loads under way, 300 to 900 cycles)
+          if (g & 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full + (g >> 1));
+          }
+          if (k + 1 < n_steps) load(g);
         }
-        if (k + 1 < n_steps) load_a();
+        if (k + 1 < n_steps) {  // the lookups of the chunks behind it, while the last scores are computed
+          note(ph ^ 1, rr);
+          rr = place(next_row, next_page);
+          prefetch(rr);
+          next_row = resolve(k + 3, next_x);
+          next_page = fetch_page(next_row);
+          next_x = fetch_idx(k + 4);
+        }
         tc_bar();  // the chunk's rows and scales, and Q's factors, are there for all
 
         // --- softmax: this thread's row against 32 heads ---
@@ -1843,12 +1875,9 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
           *reinterpret_cast<uint4*>(smem + 8 * kTcSlab + row_j * 128 + (((4 * hh + i) ^ (row_j & 7)) << 4)) =
               make_uint4(w[0], w[1], w[2], w[3]);
         }
-        fence_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
-        // the next chunk's codes, from L2 by now: behind this chunk's fences, which would wait for them
-        if (k + 1 < n_steps) load_b();
       }
 
       // --- the part's sums, and O^T out ---
@@ -1951,7 +1980,7 @@ static cudaError_t latent_f(const K8Fwd& a, void* ws, cudaStream_t st) {
   const int n = k8_ctas(a);
   count_launch();
   e = launch_pdl(k8_tc_kernel<FMT>, (unsigned)n, 384, K8Tc::kSmem, st, a, static_cast<float*>(ws));
-  if (e != cudaSuccess || n == 1) return e;
+  if (e != cudaSuccess || n == 1 || a.whole_units) return e;
   count_launch();
   return launch_pdl(k8_join_kernel<64, kLatDV>, (unsigned)n, 256, 0, st, a, static_cast<float*>(ws), n);
 }
@@ -1973,7 +2002,10 @@ static void k8_geometry(K8Fwd& a) {
   a.sel_ch = a.topk ? (int)(((long long)a.topk * a.bs + a.chunk - 1) / a.chunk) : 0;
   a.by_tpt = k8_div_of(a.tpt);
   a.by_gdiv = k8_div_of(a.gdiv);
-  a.whole_units = a.unit_rows == 64;
+  // Units of one length, and nearly as many as CTAs: one each.  Cutting them evenly would leave parts to
+  // join (131 KB each of 64 heads x 512), which costs as much as 5 chunks.
+  const long long units = (long long)a.c.T * a.hs * a.c.Hkv;
+  a.whole_units = tc && a.topk && units <= 148 && 5 * units >= 3 * 148;
   // of a unit, what it costs beside its chunks, in chunks; the most chunks that are not worth cutting
   a.over = lat ? 0 : 1;
   a.keep = lat ? 0 : 4;
