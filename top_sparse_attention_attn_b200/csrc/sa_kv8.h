@@ -57,8 +57,8 @@ struct K8Fwd {
   // chunks of a unit that selects (0: every row)
   int chunk, unit_rows, tpt, gdiv, hs, sel_ch;
   int over, keep;   // see k8_begin
-  int whole_units;  // rather a CTA per unit than parts, where that is nearly as even
-  K8Div by_tpt, by_gdiv;
+  int per_unit;     // CTAs of a unit, with an even share of it each; 0: the line is cut evenly
+  K8Div by_tpt, by_gdiv, by_ch, by_per;  // by_ch, by_per: sel_ch and per_unit
   int win;           // rows before the token's own that it sees (2^30: all)
   float scale_log2;  // scale * log2(e)
   const void* q;

@@ -185,12 +185,23 @@ __device__ __forceinline__ float* k8_part(float* ws, int n_cta, int i, int rows,
   return reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + k8_parts_at(n_cta)) + i * k8_part_floats(rows, dv);
 }
 
-// n chunks shared evenly over CTAs: the first `rem` of them have one more.
+// n chunks shared evenly over CTAs: the first `rem` of them have one more.  Or, with a.per_unit,
+// units of a.sel_ch chunks (fewer than 2^28 in all) over that many CTAs each.
 struct K8Share {
   long long base;
   int rem;
-  __device__ long long at(int i) const { return base * i + min(i, rem); }
-  __device__ int of(long long w) const {
+  __device__ long long at(const K8Fwd& a, int i) const {
+    if (a.per_unit) {
+      const int u = k8_quot(a.by_per, i);
+      return u * a.sel_ch + k8_quot(a.by_per, (i - u * a.per_unit) * a.sel_ch);
+    }
+    return base * i + min(i, rem);
+  }
+  __device__ int of(const K8Fwd& a, long long w) const {
+    if (a.per_unit) {
+      const int u = k8_quot(a.by_ch, (int)w);
+      return u * a.per_unit + k8_quot(a.by_ch, ((int)w - u * a.sel_ch + 1) * a.per_unit - 1);
+    }
     const long long head = (base + 1) * rem;
     return (int)(w < head ? w / (base + 1) : rem + (w - head) / base);
   }
@@ -296,10 +307,12 @@ __device__ __forceinline__ bool k8_begin(const K8Fwd& a, float* ws, int tid, K8F
     if (x < warp) at += f.sum[x];
   }
   int n_cta = (int)min(W, (long long)gridDim.x);  // a share is empty only in CTAs behind these
-  if (a.whole_units) n_cta = (int)min(W / a.sel_ch, (long long)n_cta);  // a CTA each
+  if (a.per_unit) n_cta = min(k8_quot(a.by_ch, (int)min(W, 148ll * a.sel_ch)) * a.per_unit, (int)gridDim.x);
   if (tid < 2) (reinterpret_cast<K8Join*>(ws) + 2 * blockIdx.x)[tid].n = 0;
   if (blockIdx.x >= n_cta) return false;
-  if (W <= 0x7fffffff) {
+  if (a.per_unit) {
+    cur.share.base = cur.share.rem = 0;
+  } else if (W <= 0x7fffffff) {
     cur.share.base = k8_udiv((uint32_t)W, (uint32_t)n_cta);
     cur.share.rem = (int)((uint32_t)W - (uint32_t)cur.share.base * (uint32_t)n_cta);
   } else {
@@ -309,7 +322,7 @@ __device__ __forceinline__ bool k8_begin(const K8Fwd& a, float* ws, int tid, K8F
   // This share's two ends, each put where a unit can be cut: not within its first a.over, and not at
   // all in a unit of up to a.keep chunks while a CTA has such a unit or more.  (Both CTAs at
   // an end see it alike.)
-  const long long ends[2] = {cur.share.at(blockIdx.x), cur.share.at(blockIdx.x + 1)};
+  const long long ends[2] = {cur.share.at(a, blockIdx.x), cur.share.at(a, blockIdx.x + 1)};
   if (tid == 0 && ends[1] >= W) f.w1 = W;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -372,8 +385,8 @@ __device__ __forceinline__ void k8_next(K8Cursor& c) {
 __device__ __forceinline__ void k8_note(const K8Fwd& a, float* ws, const K8Share& share, long long begin, int c0, int len,
                                         int t, int head, int rows, int gdiv) {
   K8Join jn;
-  jn.first = c0 == 0 ? (int)blockIdx.x : share.of(begin + a.over);
-  jn.n = share.of(begin + len - 1) - jn.first + 1;
+  jn.first = c0 == 0 ? (int)blockIdx.x : share.of(a, begin + a.over);
+  jn.n = share.of(a, begin + len - 1) - jn.first + 1;
   jn.t = t;
   jn.head = head;
   jn.rows = rows;
@@ -1013,7 +1026,7 @@ static bool k8_latent(const K8Fwd& a) { return a.c.dqk > 192; }
 
 // CTAs: all that the SMs hold at once, or as many as the longest possible line has chunks.
 static int k8_ctas(const K8Fwd& a) {
-  if (a.whole_units) return a.c.T * a.hs * a.c.Hkv;
+  if (a.per_unit) return a.c.T * a.hs * a.c.Hkv * a.per_unit;
   const int occ = k8_latent(a) ? 1 : a.c.dqk + a.c.dv <= 128 ? 4 : (a.c.dqk <= 128 ? 3 : 2);
   const long long units = ((long long)(a.c.T + a.tpt - 1) / a.tpt + (a.tpt > 1 ? min(a.c.B, a.c.T) : 0)) * a.hs * a.c.Hkv;
   long long ch = a.sel_ch;
@@ -1966,7 +1979,7 @@ static cudaError_t latent_t(const K8Fwd& a, void* ws, cudaStream_t st) {
   const int n = k8_ctas(a);
   count_launch();
   e = launch_pdl(k, (unsigned)n, 256, P::kSmem, st, a, static_cast<float*>(ws));
-  if (e != cudaSuccess || n == 1) return e;
+  if (e != cudaSuccess || n == 1 || a.per_unit == 1) return e;
   count_launch();
   return launch_pdl(k8_join_kernel<MT * 16, kLatDV>, (unsigned)n, 256, 0, st, a, static_cast<float*>(ws), n);
 }
@@ -1980,7 +1993,7 @@ static cudaError_t latent_f(const K8Fwd& a, void* ws, cudaStream_t st) {
   const int n = k8_ctas(a);
   count_launch();
   e = launch_pdl(k8_tc_kernel<FMT>, (unsigned)n, 384, K8Tc::kSmem, st, a, static_cast<float*>(ws));
-  if (e != cudaSuccess || n == 1 || a.whole_units) return e;
+  if (e != cudaSuccess || n == 1 || a.per_unit == 1) return e;
   count_launch();
   return launch_pdl(k8_join_kernel<64, kLatDV>, (unsigned)n, 256, 0, st, a, static_cast<float*>(ws), n);
 }
@@ -2002,10 +2015,13 @@ static void k8_geometry(K8Fwd& a) {
   a.sel_ch = a.topk ? (int)(((long long)a.topk * a.bs + a.chunk - 1) / a.chunk) : 0;
   a.by_tpt = k8_div_of(a.tpt);
   a.by_gdiv = k8_div_of(a.gdiv);
-  // Units of one length, and nearly as many as CTAs: one each.  Cutting them evenly would leave parts to
-  // join (131 KB each of 64 heads x 512), which costs as much as 5 chunks.
+  // Units of one length, and no more than SMs: as many CTAs each as there are, of which none has parts of two
+  // units.  A part's start, end and join (131 KB of 64 heads x 512) cost as much as 5 chunks of 64 heads.  With 2048 rows:
+  // 37 against 45 us of the even cut (48 tokens, 16 heads), 59 against 71 (40, 64), 91 against 106 (48, 128).
   const long long units = (long long)a.c.T * a.hs * a.c.Hkv;
-  a.whole_units = tc && a.topk && units <= 148 && 5 * units >= 3 * 148;
+  a.per_unit = lat && a.topk && units <= 148 && a.sel_ch < 1 << 20 ? min(148 / (int)units, a.sel_ch) : 0;
+  a.by_ch = k8_div_of(max(a.sel_ch, 1));
+  a.by_per = k8_div_of(max(a.per_unit, 1));
   // of a unit, what it costs beside its chunks, in chunks; the most chunks that are not worth cutting
   a.over = lat ? 0 : 1;
   a.keep = lat ? 0 : 4;
