@@ -1073,14 +1073,16 @@ static cudaError_t split_d(const K8Fwd& a, void* ws, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 // a shared row of 576 columns, V its first 512
 // ---------------------------------------------------------------------------
-// Up to 32 heads (more: the next section).  A unit is one token and 16 MT of its heads, MT = 1
-// or 2; 64 rows per chunk and one CTA of 8 warps per SM, on the same line of chunks as
-// above.  The rows, selected one by one, are copied whole (cp.async, three stages), and serve
-// as K and V.  For the scores warp (mg, tg) takes 16 of the heads against its share of the rows;
-// for O a warp takes all heads against 64 of the columns.  P goes through shared memory
-// between the two.  The running maximum is shared by the CTA and looked at with the
-// barrier that the stages need anyway; it is exchanged only when some row's grew by more
-// than 2^kK8Grow.
+// Up to 32 heads at a time (more than 32, where there is work for it: the next section).  A unit
+// is one token and 16 MT of its heads, MT = 1 or 2; 64 rows per chunk and one CTA of 8 warps per
+// SM, on the same line of chunks as above.  The rows, selected one by one, are copied whole
+// (cp.async, three stages), and serve as K and V.  For the scores warp (mg, tg) takes 16 of the
+// heads against its share of the rows; for O a warp takes all heads against 64 of the columns.  P
+// goes through shared memory between the two.  The running maximum is shared by the CTA and
+// looked at with the barrier that the stages need anyway; it is exchanged only when some row's
+// grew by more than 2^kK8Grow.
+// Measured: 48 tokens x 16 heads x 2048 rows 37 us, a token x 128 heads x 2048 rows 16.5.  Bound by
+// a chunk's dependent steps (stage, scores, P, O) in the one CTA that fits an SM.
 constexpr int kLatRows = 64, kLatDK = 576, kLatDV = 512;
 
 template <int MT>
@@ -1485,17 +1487,21 @@ __global__ void __launch_bounds__(256, 1) k8_latent_kernel(const __grid_constant
 // so that K is converted once and serves both products, O stays in TMEM (256 columns) and a
 // thread holds a row's scores.  Shared memory holds one chunk as halves (147 KB, 9 slabs of
 // 64 columns) and Q (74 KB); P^T takes the slab of the last 64 columns, which only the scores
-// need.  Eight warps fetch the next chunk's codes into registers, convert them slab by
-// slab as the MMAs of the chunk before let go of the slabs, and do the softmax; a ninth
-// issues (of a third warpgroup, which gives its registers to the other two).  Bound: the MMAs, 36 + 32 at N = 64 and 44.5 cycles each (3026 per chunk), and the
-// softmax between the two products, which nothing overlaps.
+// need.  Eight warps convert a chunk's codes from registers, slab by slab as the MMAs of the
+// chunk before let go of the slabs, ask for the next chunk's in their place, and do the softmax;
+// a ninth issues (of a third warpgroup, which gives its registers to the other two).
+// Measured: 48 tokens x 128 heads x 2048 rows 96 us, of which a part's start (lookups of four
+// dependent loads, Q, the first conversions) is 10 and its end 5.  A chunk takes some 7600 cycles:
+// conversion 3600 (its stores of 147 KB and the operands of the 68 MMAs, 6 KB each at N = 64, share
+// shared memory's 128 bytes a cycle), the last scores 2100, softmax 1600, of which only
+// O and the first scores overlap with the conversion.  The conversion's arithmetic is 4 % of it all.
 constexpr int kTcRows = 128, kTcSlab = kTcRows * 128, kTcSlabs = 9;
 struct K8Tc {
   static constexpr int kQAt = kTcSlabs * kTcSlab;
   static constexpr int kMetaAt = kQAt + 9 * 64 * 128;       // [2][128] rows seen, [2][128] scales
   static constexpr int kHeadAt = kMetaAt + 2 * kTcRows * 8;  // [64] (fr, base)
   static constexpr int kRedAt = kHeadAt + 64 * 8;            // [4][64]
-  static constexpr int kBarAt = kRedAt + 4 * 64 * 4;         // full [2], p_full, s_done, free [4]
+  static constexpr int kBarAt = kRedAt + 4 * 64 * 4;         // full [2], p_full, s_done, free [4], drained
   static constexpr int kSmem = kBarAt + 16 * 8 + 1024;
   static constexpr uint32_t kTmemS = 256;  // column of S^T behind the four blocks of O^T
 };
@@ -1553,10 +1559,10 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
   const K8Cache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + P::kBarAt);
-  uint64_t *const p_full = full + 2, *const s_done = full + 3, *const blk_free = full + 4;
+  uint64_t *const p_full = full + 2, *const s_done = full + 3, *const blk_free = full + 4, *const drained = full + 8;
   if (tid == 0) {
     for (int i = 0; i < 3; ++i) mbar_init(full + i, 8);
-    for (int i = 3; i < 8; ++i) mbar_init(full + i, 1);
+    for (int i = 3; i < 9; ++i) mbar_init(full + i, 1);
     mbar_fence_init();
     abort_word = 0;
   }
@@ -1584,27 +1590,29 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
       const uint32_t dv = (uint32_t)sdesc(kat, kTcSlab, 1024), dp = (uint32_t)sdesc(pat, kTcSlab, 1024);
       const uint32_t hi = (uint32_t)(sdesc(0, 0, 1024) >> 32);
       constexpr uint32_t id_s = k8_idesc(128, 64, false, false), id_o = k8_idesc(128, 64, true, true);
+      // A wait that gave up changes nothing here (the later ones return at once, the products are not used):
+      // the warp stays together, as electing asks for.
       for (long long n = 0; n < n_chunks; ++n) {
         const uint32_t ph = (uint32_t)(n & 1);
-        bool ok = true;
         // Unrolled with constant offsets from bases that the compiler sees to be alike in the whole warp, so that
         // a descriptor takes one addition in the warp's own registers; 32 bits of it, the others never change.
-        // (Additions carried from MMA to MMA took 120 to 170 cycles each, one thread's registers 8 % more.)
+        // (Additions carried from MMA to MMA took 120 to 170 cycles each, one thread's registers 2 % of the call.)
 #pragma unroll
         for (int sl = 0; sl < kTcSlabs; ++sl) {
           if ((sl & 3) == 0 && sl < 8) {  // four slabs, then five: a wait and its fence cost 300 to 500 cycles
-            ok = ok && mbar_wait(full + (sl >> 2), ph, &abort_word, c.status);
-            fence_async_smem();
+            mbar_wait(full + (sl >> 2), ph, &abort_word, c.status);
+            fence_async_smem();  // the converting warps' stores, seen through the barrier, before the MMAs' reads
             tc_fence_after();
           }
           if (tc_elect()) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            tc_mma(tmem + P::kTmemS, dk + ((sl * kTcSlab + 32 * e) >> 4), dq + ((sl * 8192 + 32 * e) >> 4), hi, id_s, sl || e);
-          if (sl == kTcSlabs - 1) mma_commit(s_done);
+            for (int e = 0; e < 4; ++e)
+              tc_mma(tmem + P::kTmemS, dk + ((sl * kTcSlab + 32 * e) >> 4), dq + ((sl * 8192 + 32 * e) >> 4), hi, id_s,
+                     sl || e);
+            if (sl == kTcSlabs - 1) mma_commit(s_done);
           }
         }
-        if (!ok || !mbar_wait(p_full, ph, &abort_word, c.status)) break;
+        mbar_wait(p_full, ph, &abort_word, c.status);
         fence_async_smem();
         tc_fence_after();
         const uint32_t over = *(volatile int*)&fresh;
@@ -1612,13 +1620,15 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
         for (int mb = 0; mb < 4; ++mb) {
           if (tc_elect()) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            tc_mma(tmem + mb * 64, dv + ((mb * 2 * kTcSlab + 2048 * e) >> 4), dp + ((2048 * e) >> 4), hi, id_o, !over || e);
-          mma_commit(blk_free + mb);
+            for (int e = 0; e < 8; ++e)
+              tc_mma(tmem + mb * 64, dv + ((mb * 2 * kTcSlab + 2048 * e) >> 4), dp + ((2048 * e) >> 4), hi, id_o,
+                     !over || e);
+            mma_commit(blk_free + mb);
           }
         }
       }
-      if (abort_word) mbar_wait_drain(blk_free + 3, 0);  // bounded: what was issued before the wait gave up
+      if (tc_elect()) mma_commit(drained);  // the workers that gave up did not wait for the last products
+      mbar_wait_drain(drained, 0);
     }
     __syncwarp();
   } else {
@@ -2003,7 +2013,7 @@ static void k8_geometry(K8Fwd& a) {
   // More than 32 heads of a shared row go to the tcgen05 kernel (64 heads x 128 rows a step; it reads codes
   // 32 bytes at a time), but not where shares of 32 heads x 64 rows leave SMs idle: its start and end cost
   // 13 us more.  There mma.sync took 16.5 us against 29 (a token, 2048 rows, 128 heads), 11.7 against 20.5
-  // (4 tokens, 36 rows); beyond, 142 against 105 (48 tokens, 2048 rows), 30 against 26.4 (8 tokens, 1024).
+  // (4 tokens, 36 rows); beyond, 142 against 96 (48 tokens, 2048 rows), 30 against 26.4 (8 tokens, 1024).
   const long long small = (long long)a.c.T * a.c.Hkv * ((a.G + 31) / 32) *
                           (a.topk ? ((long long)a.topk * a.bs + 63) / 64 : ((long long)a.c.max_pages * a.c.ps + 63) / 64);
   const bool tc = a.G > 32 && small > 148 && ((uintptr_t)a.c.k & 31) == 0;
@@ -2017,7 +2027,7 @@ static void k8_geometry(K8Fwd& a) {
   a.by_gdiv = k8_div_of(a.gdiv);
   // Units of one length, and no more than SMs: as many CTAs each as there are, of which none has parts of two
   // units.  A part's start, end and join (131 KB of 64 heads x 512) cost as much as 5 chunks of 64 heads.  With 2048 rows:
-  // 37 against 45 us of the even cut (48 tokens, 16 heads), 59 against 71 (40, 64), 91 against 106 (48, 128).
+  // 37 against 45 us of the even cut (48 tokens, 16 heads), 59 against 71 (40, 64), 96 against 106 (48, 128).
   const long long units = (long long)a.c.T * a.hs * a.c.Hkv;
   a.per_unit = lat && a.topk && units <= 148 && a.sel_ch < 1 << 20 ? min(148 / (int)units, a.sel_ch) : 0;
   a.by_ch = k8_div_of(max(a.sel_ch, 1));
