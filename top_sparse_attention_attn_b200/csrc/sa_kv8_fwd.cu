@@ -39,6 +39,9 @@ bool k8_built(int dqk, int dv, bool shared) {
 // exponential, and its 11 bits sit where the products are largest whatever the pages'
 // scales are.  p' <= 2^15: the maximum is held at 2^7 and let grow by up to 2^8 before O is
 // rescaled; halves reach 2^-31 of the held one.
+// Measured: 32 requests of 8 k to 32 k rows, 64 / 8 heads of 128 / 128, 1.32 GB: 255 to 271 us,
+// 4.9 to 5.2 TB/s of a copy's 6.55; bound by the issue slots close behind memory.  16 requests of
+// up to 8 k rows: 43 us, of which start and join are 16.  One of 65536 rows, 4 heads of 192 / 128: 31.
 constexpr int kK8Warps = 4;
 constexpr int kK8Chunk = 32 * kK8Warps;
 constexpr float kK8Grow = 8.f, kK8Top = 7.f;

@@ -15,7 +15,7 @@ namespace sa {
 // from L2) into two prefix arrays in shared memory, tokens and new pages, and then
 // looks up its share of the tokens and new pages there by bisection; block 0 writes
 // the per-request outputs.  The scan repeated per block costs less than a second
-// launch that would wait for it.
+// launch that would wait for it.  Bound by latency: 6.4 us for 64 requests, 7.2 for 1500.
 __device__ __forceinline__ int plan_upper(const int* a, int n, int x) {  // largest b < n with a[b] <= x
   int lo = 0, hi = n - 1;
   while (lo < hi) {
@@ -317,7 +317,8 @@ __device__ __forceinline__ int k8_find_warp(const K8Cache& c, int t, int lane) {
 // Where requests bring many rows, a CTA takes a run, a head, and K or V: the first threads
 // of the grid's x range find run x over the requests' page counts.  Bound by the bytes (2
 // in, 1 out per element) and, a run at a time, by the chain offsets -> rows -> maximum ->
-// codes; CTAs enough that an SM holds several.
+// codes; CTAs enough that an SM holds several.  10 k tokens of 7 prompts, 4 heads of 192 / 128:
+// 13.1 us, 2.9 TB/s.
 template <bool F16, int NT>
 __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 6) kv8_write_runs_kernel(const __grid_constant__ K8Write a) {
   __shared__ float red[NT / 32];
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 6) kv8_write_runs_kernel(c
 
 // Where they bring a few rows each, a CTA takes the runs that begin in its window of
 // tokens (one token, unless there are many), NT threads for K and as many for V.  Bound by
-// the chain offsets -> length -> table -> scale.
+// the chain offsets -> length -> table -> scale: 3.3 us for 64 tokens of 8 heads of 128 / 128.
 template <bool F16, int NT, bool SHARED>
 __global__ void __launch_bounds__(SHARED ? NT : 2 * NT, 8) kv8_write_kernel(const __grid_constant__ K8Write a) {
   __shared__ float red[2][NT / 32];
@@ -426,7 +427,7 @@ cudaError_t launch_kv8_write(K8Write a, cudaStream_t st) {
   a.by_k = k8_div_of(c.dqk / 8);
   a.by_v = k8_div_of(c.dv / 8);
   // 8 rows per request on average: 10 k tokens of 7 prompts, 4 heads of 192 / 128, took 31 us
-  // window by window
+  // window by window, 13 run by run
   if (c.T >= 8ll * c.B) {
     const dim3 grid((unsigned)(c.T / c.ps + 2 * c.B), (unsigned)c.Hkv, c.shared ? 1 : 2);
     const auto k = c.dqk > 192 ? (a.f16 ? kv8_write_runs_kernel<true, 512> : kv8_write_runs_kernel<false, 512>)
