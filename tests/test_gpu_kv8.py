@@ -267,6 +267,24 @@ def test_rows_behind_the_last_sequence_stay(topk):
     assert (o[3:] == 7).all() and (lse[3:] == 7).all() and cache.read_status() == L.SA_OK
 
 
+@pytest.mark.parametrize("heads,T,topk", [(16, 8, 300), (128, 8, 300), (64, 40, 200), (16, 200, 100), (128, 9, 40)])
+def test_latent_rows_behind_the_last_sequence_stay(heads, T, topk):
+    """The CTAs are shared out for T tokens, three of which there are."""
+    rng = np.random.default_rng(61)
+    lens, cu = [400, 90], [0, 2, 3]
+    cache, table, kf, vf = make_cache(rng, lens, page=64, H=1, dqk=576, dv=512, shared=True)
+    q = torch.randn((T, heads, 576), device="cuda").to(torch.bfloat16)
+    q[3:] = float("nan")
+    o = torch.full((T, heads, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, heads), 7.0, device="cuda")
+    idx = np.full((T, 1, topk), 1 << 30)
+    idx[:3] = make_idx(rng, lens, [2, 1], 1, 1, topk)
+    cache.attend(q, _i32(table), _i32(lens), cu_seqlens_q=_i32(cu), o=o, lse=lse, idx=_i32(idx))
+    ref = R.attend(q[:3].double().cpu().numpy(), kf, vf, table, lens, cu, 64, 576 ** -0.5, idx=idx[:3])
+    check("latent padded", o[:3], lse[:3], ref, q.dtype, 576, 400)
+    assert (o[3:] == 7).all() and (lse[3:] == 7).all() and cache.read_status() == L.SA_OK
+
+
 @pytest.mark.parametrize("name", ["chunk", "window", "blocks", "latent_rows", "latents_rows", "latents_all",
                                   "page7"])
 def test_rows_that_are_not_seen_may_hold_anything(name):
