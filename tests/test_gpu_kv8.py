@@ -430,6 +430,25 @@ def test_offsets_past_32_bits():
     check("far pages", o, lse, ref, q.dtype, d, 300)
 
 
+@pytest.mark.parametrize("B", [0, 2])
+@pytest.mark.parametrize("shared,dqk,dv", [(False, 128, 128), (True, 128, 128), (True, 576, 512)])
+@pytest.mark.parametrize("topk", [0, 64])
+def test_a_step_without_tokens(shared, dqk, dv, topk, B):
+    cache = Kv8Cache.empty(4, 16, 1, dqk, dv, shared=shared)
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    table, lens, cu = z(B, 2), z(B), z(B + 1)
+    q = torch.empty((0, 64, dqk), dtype=torch.bfloat16, device="cuda")
+    idx = z(0, 1, topk) if topk else None
+    o, lse = cache.attend(q, table, lens, cu_seqlens_q=cu, idx=idx)
+    assert o.shape == (0, 64, dv) and lse.shape == (0, 64)
+    cache.write(q[:, :1], None if shared else q[:, :1, :dv].contiguous(), table, lens, cu_seqlens_q=cu)
+    # sequences without tokens, one layout after the other
+    o, lse = cache.attend(q.view(B, 0, 64, dqk), table, lens, idx=None if idx is None else idx.view(B, 0, 1, topk))
+    assert o.shape == (B, 0, 64, dv)
+    torch.cuda.synchronize()
+    assert cache.read_status() == L.SA_OK and int(cache.k.view(torch.uint8).max()) == 0
+
+
 # ---- write --------------------------------------------------------------------
 
 WRITES = {

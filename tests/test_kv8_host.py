@@ -2,6 +2,9 @@
 against independent computations, and the refusals of the C ABI and of the wrapper."""
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -11,6 +14,7 @@ from oracle import kv8_ref as R
 from top_sparse_attention_attn_b200 import Kv8Cache, plan_pages
 from top_sparse_attention_attn_b200 import _lib as L
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 0x10000  # 16-byte aligned, never dereferenced: these calls fail validation first
 
 
@@ -143,6 +147,29 @@ def test_workspace_and_null_arguments_are_refused():
     assert lib.sa_kv8_fwd(ctypes.byref(_cache(t_q=0)), ctypes.byref(_query()), None, 0, None) == L.SA_OK
     assert lib.sa_kv8_write(ctypes.byref(_cache(t_q=0)), ctypes.byref(L.SaKv8Rows(k_stride=256, v_stride=256)),
                             None) == L.SA_OK
+
+
+EMPTY_STEPS = """
+import ctypes
+from tests.test_kv8_host import FAKE, L, _cache, _query
+r, lib = ctypes.byref, L.lib()
+for shared, d, dv in [(0, 64, 64), (0, 128, 128), (0, 192, 128), (1, 128, 128), (1, 576, 512)]:
+    for empty in [dict(t_q=0), dict(batch=0), dict(layout=0, s_q=0), dict(layout=0, s_q=3, batch=0)]:
+        for topk in [0, 64]:
+            print(shared, d, dv, empty, topk, flush=True)
+            c = _cache(kv_shared=shared, d_qk=d, d_v=dv, **empty)
+            q, n = _query(q_stride=8 * d, topk=topk, idx=FAKE), ctypes.c_size_t(7)
+            assert lib.sa_kv8_fwd_get_workspace_size(r(c), r(q), r(n)) == L.SA_OK and n.value == 0
+            assert lib.sa_kv8_fwd(r(c), r(q), None, 0, None) == L.SA_OK
+            w = L.SaKv8Rows(k_stride=2 * d, v_stride=2 * dv)
+            assert lib.sa_kv8_write(r(c), r(w), None) == L.SA_OK
+"""
+
+
+def test_a_step_without_tokens_or_requests_asks_for_nothing():
+    """In a process of its own: arithmetic on a count of zero ends the process that it happens in."""
+    r = subprocess.run([sys.executable, "-c", EMPTY_STEPS], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, (r.returncode, r.stdout[-200:], r.stderr[-500:])
 
 
 @pytest.mark.parametrize("kw,status", [

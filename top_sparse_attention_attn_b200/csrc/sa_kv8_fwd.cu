@@ -2041,6 +2041,7 @@ static void k8_geometry(K8Fwd& a) {
 }
 
 size_t k8_fwd_workspace(K8Fwd a) {
+  if (a.c.T == 0 || a.c.B == 0) return 0;  // nothing is launched, and there is no unit to share the CTAs out to
   k8_geometry(a);
   const int n = k8_ctas(a);
   return k8_parts_at(n) + (size_t)n * 2 * k8_part_floats(a.unit_rows, a.c.dv) * sizeof(float);
