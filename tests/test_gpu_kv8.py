@@ -522,6 +522,48 @@ def test_write_bsnd_strided_and_padded():
                  lambda: cache.write(kd, kd, _i32(table), _i32(c["lens"]), cu_seqlens_q=_i32([0, 1, 3])))
 
 
+@pytest.mark.parametrize("first", [1, 3, 5, 300])
+@pytest.mark.parametrize("B,lo,hi,H,d", [(5, 1, 3, 2, 128), (300, 5, 7, 8, 64), (300, 1, 9, 3, 64), (4, 20, 90, 2, 128)])
+def test_write_of_a_slice_of_a_step(B, lo, hi, H, d, first):
+    """Offsets that begin behind 0: a part of a larger step's sequences, with its packed tokens whole.  Few rows
+    per request in windows of one and of several tokens, and many."""
+    rng = np.random.default_rng(24 + first)
+    new = rng.integers(lo, hi + 1, B)
+    lens = (new + rng.integers(0, 40, B)).tolist()
+    c = dict(lens=lens, new=new, H=H, dqk=d, dv=d, fmt="e4m3", shared=False)
+    cache, table, _, _ = make_cache(rng, lens, page=16, H=H, dqk=d, dv=d)
+    cu = first + np.concatenate([[0], np.cumsum(new)])
+    k, v = (torch.from_numpy(rng.standard_normal((cu[-1] + 4, H, d))).to(torch.bfloat16) for _ in range(2))
+    kd, vd = k.cuda(), v.cuda()
+    _check_write(c, cache, table, k, v, cu,
+                 lambda: cache.write(kd, vd, _i32(table), _i32(lens), cu_seqlens_q=_i32(cu)))
+
+
+def test_a_step_served_in_two_slices():
+    """The plan of a step, written and attended to a part of its requests at a time: as in one call, bit by bit."""
+    rng = np.random.default_rng(25)
+    B, H, d, page, cut = 600, 8, 64, 16, 217
+    new = rng.integers(1, 8, B)
+    T = int(new.sum())
+    k, v, q = (torch.from_numpy(rng.standard_normal((T, h, d))).to(torch.bfloat16).cuda() for h in (H, H, 2 * H))
+    out = []
+    for parts in ([(0, B)], [(0, cut), (cut, B)]):
+        cache = Kv8Cache.empty(B, page, H, d, d)
+        table = _i32(np.full((B, 1), -1))
+        p = plan_pages(_i32([0] * B), _i32(new), table, _i32(np.arange(B)), _i32([B]), page_size=page, n_tokens=T)
+        o, lse = torch.zeros_like(q), torch.zeros((T, 2 * H), device="cuda")
+        for a, b in parts:
+            s = dict(block_table=table[a:b], seq_lens=p.seq_lens[a:b], cu_seqlens_q=p.cu_seqlens_q[a:b + 1])
+            cache.write(k, v, **s)
+            cache.attend(q, **s, o=o, lse=lse)
+        out.append((o, lse, cache))
+    (o, lse, one), (o2, lse2, two) = out
+    same = {n: torch.equal(getattr(one, n).view(torch.uint8), getattr(two, n).view(torch.uint8))
+            for n in ("k", "v", "k_scale", "v_scale")}
+    assert all(same.values()), same
+    assert int(p.n_served) == B and torch.equal(o, o2) and torch.equal(lse, lse2) and lse.all()
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_write_of_infinities_nan_and_extremes(fmt):
     rng = np.random.default_rng(22)

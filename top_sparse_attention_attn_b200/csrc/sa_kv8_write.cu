@@ -394,16 +394,13 @@ __global__ void __launch_bounds__(SHARED ? NT : 2 * NT, 8) kv8_write_kernel(cons
   const int t_end = min(t + a.window, c.T);
   int b = k8_find_warp(c, t, threadIdx.x & 31);
   K8Seq s = k8_seq(c, b);
+  t = max(t, s.t0);  // tokens before the first sequence are no sequence's
   while (t < t_end) {
     while (t >= s.t0 + s.n) {  // behind this sequence (or behind an empty one)
       if (++b >= c.B) return;
       s = k8_seq(c, b);
-      if (s.t0 > t) t = s.t0;  // offsets that leave a gap: no sequence's tokens
-      if (t >= t_end) return;
     }
-    const int i = t - s.t0;
-    if (i < 0) return;  // offsets out of order
-    const int pos = s.first + i;
+    const int i = t - s.t0, pos = s.first + i;  // i >= 0: a sequence begins where the one before ends, or earlier
     if (pos < 0) {
       t -= pos;
       continue;
