@@ -257,6 +257,24 @@ def test_wrapper_refuses_wrong_types_shapes_and_strides():
         c.write(k, k, **s)
 
 
+def test_empty_tensors_may_have_any_strides():
+    """Without elements a tensor is contiguous whatever its strides: the checks pass, up to the one for a GPU."""
+    c = _cpu_cache()
+    none = torch.zeros(0, dtype=torch.int32)
+    table = torch.tensor(np.zeros((0, 4)), dtype=torch.int32)
+    assert table.stride() == (0, 0)
+    s = dict(block_table=table, seq_lens=none, cu_seqlens_q=torch.zeros(1, dtype=torch.int32))
+    x = torch.tensor(np.zeros((0, 2, 128)), dtype=torch.bfloat16)
+    q = torch.zeros((128, 8, 5), dtype=torch.bfloat16).transpose(0, 2)[:0]
+    for cols in (table, torch.zeros((3, 8), dtype=torch.int32).t()[:0, :3]):
+        with pytest.raises(ValueError, match="CUDA"):
+            c.attend(q, **{**s, "block_table": cols})
+        with pytest.raises(ValueError, match="CUDA"):
+            c.write(x, x, **{**s, "block_table": cols})
+        with pytest.raises(ValueError, match="CUDA"):
+            plan_pages(none, none, cols, none, torch.zeros(1, dtype=torch.int32), page_size=16, n_tokens=0)
+
+
 def test_cache_refuses_tensors_that_do_not_fit():
     k = torch.zeros((6, 16, 2, 128), dtype=torch.int8)
     sc = torch.zeros((6, 2))

@@ -81,6 +81,7 @@ Table table_of(PyObject* o, int index) {
   const at::Tensor& t = tensor(o, "block_table");
   if (t.scalar_type() != at::kInt || t.dim() != 2) type_error("block_table: int32 [B, max_pages] expected");
   check_device(t, "block_table", index);
+  if (t.numel() == 0) return {static_cast<int32_t*>(t.data_ptr()), t.size(0), t.size(1), t.size(1)};
   if (t.size(1) > 1 && t.stride(1) != 1) value_error("block_table rows are not contiguous");
   const int64_t row = t.size(0) > 1 ? t.stride(0) : t.size(1);
   if (row < t.size(1)) value_error("block_table rows overlap");
@@ -95,9 +96,10 @@ int64_t token_step(const at::Tensor& t, const char* name, int64_t heads, int64_t
   if ((n != 3 && n != 4) || t.size(n - 2) != heads || t.size(n - 1) != d)
     value_error(std::string(name) + " has shape " + shape_text(t.sizes()) + ": [T, " + std::to_string(heads) + ", " +
                 std::to_string(d) + "] or [B, s, " + std::to_string(heads) + ", " + std::to_string(d) + "] expected");
+  int64_t step = heads * d;
+  if (t.numel() == 0) return step;  // no element lies anywhere
   if ((d > 1 && t.stride(n - 1) != 1) || (heads > 1 && t.stride(n - 2) != d))
     value_error(std::string(name) + ": a token's rows are not contiguous");
-  int64_t step = heads * d;
   if (n == 3) {
     if (t.size(0) > 1) step = t.stride(0);
   } else if (t.size(1) > 1) {
