@@ -586,6 +586,17 @@ sa_status sa_selftest_gather4(const void* src, int32_t rows, int32_t cols, const
  * wait (wrongly) completed, else 0.  Asynchronous; takes as long as the limit. */
 sa_status sa_selftest_wait_timeout(int32_t* status, int32_t* waited, void* stream);
 
+/* Self-check of what a wait that gave up leaves behind in sa_kv8_fwd's tcgen05
+ * kernel: sa_kv8_fwd in which, in every CTA, one wait of one warp at one of the
+ * CTA's chunks completes as ever but counts as given up.  warp 8 (which issues
+ * the products): wait 0 and 1 (a chunk's halves), 2 (the probabilities); warps 0
+ * to 7: wait 3 to 6 (a part of shared memory, not at chunk 0), 7 (the scores), 8
+ * (a unit's last products, at its last chunk).  Where it happens the unit at hand
+ * and the CTA's later ones become NaN and the status word gets the timeout bit.
+ * SA_ERR_UNSUPPORTED where sa_kv8_fwd takes another kernel, or for integer codes. */
+sa_status sa_selftest_kv8_give_up(const sa_kv8_cache* cache, const sa_kv8_query* query, int32_t warp, int32_t wait,
+                                  int32_t chunk, void* ws, size_t ws_bytes, void* stream);
+
 /* Which kernels sa_fwd and sa_bwd would run for `args` (validated as by
  * *_get_workspace_size).  Either output pointer may be NULL.  Host only. */
 sa_status sa_plan(const sa_args* args, int32_t* fwd_kernel, int32_t* bwd_kernel);

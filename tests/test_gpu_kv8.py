@@ -9,6 +9,8 @@ and lse by d_z + 2^-22 (1 + |lse|), where d_z covers fp32 sums of d products, (d
 times scale sum |q||k|, plus 2^-20 for the exponential and the query held as fp16 times a
 power of two (11 bits hold bf16 and fp16 values; what is lost lies 2^-30 below the largest)."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -428,6 +430,46 @@ def test_offsets_past_32_bits():
     o, lse = cache.attend(q, _i32(table), _i32(lens), cu_seqlens_q=_i32(cu))
     ref = R.attend(q.double().cpu().numpy(), kf, vf, local, lens, cu, page, d ** -0.5)
     check("far pages", o, lse, ref, q.dtype, d, 300)
+
+
+@pytest.mark.parametrize("warp,wait,chunk", [(8, 0, 0), (8, 1, 0), (8, 2, 0), (8, 0, 3), (8, 1, 2), (8, 2, 1), (3, 3, 1),
+                                             (0, 4, 2), (7, 5, 3), (5, 6, 1), (1, 7, 0), (6, 7, 3), (2, 8, 1), (7, 8, 3)])
+def test_a_wait_that_gave_up_makes_its_units_nan(warp, wait, chunk):
+    """The tensor-memory kernel: whichever warp's wait it was, the unit at hand and the share's later ones are NaN,
+    and all others as ever."""
+    rng = np.random.default_rng(54)
+    lens, new, topk = [400, 200, 700], [60, 60, 40], 130
+    T, n_cta, ch = sum(new), 148, 2                        # a unit: 64 heads of a token, 130 rows in chunks of 128
+    cache, table, _, _ = make_cache(rng, lens, page=64, H=1, dqk=576, dv=512, shared=True)
+    idx = _i32(make_idx(rng, lens, new, 1, 1, topk))
+    tab, ln, cu = _i32(table), _i32(lens), _i32(np.concatenate([[0], np.cumsum(new)]))
+    q = torch.randn((T, 128, 576), device="cuda").to(torch.bfloat16)
+    o, lse = cache.attend(q, tab, ln, cu_seqlens_q=cu, idx=idx)
+    c, a = L.SaKv8Cache.from_buffer_copy(cache._c), L.SaKv8Query()
+    c.layout, c.t_q, c.batch, c.max_pages, c.table_stride = L.SA_LAYOUT_TND, T, 3, table.shape[1], table.shape[1]
+    c.block_table, c.seq_lens, c.cu_seqlens_q = tab.data_ptr(), ln.data_ptr(), cu.data_ptr()
+    a.dtype, a.n_heads_q, a.block_size, a.topk, a.win_left, a.scale = L.SA_DTYPE_BF16, 128, 1, topk, -1, 576 ** -0.5
+    a.q, a.q_stride, a.idx = q.data_ptr(), 128 * 576, idx.data_ptr()
+    o2, lse2 = torch.zeros_like(o), torch.zeros_like(lse)
+    a.o, a.lse = o2.data_ptr(), lse2.data_ptr()
+    r, n = ctypes.byref, ctypes.c_size_t(0)
+    assert L.lib().sa_kv8_fwd_get_workspace_size(r(c), r(a), r(n)) == L.SA_OK
+    ws = torch.zeros(n.value, dtype=torch.uint8, device="cuda")
+    assert L.lib().sa_selftest_kv8_give_up(r(c), r(a), warp, wait, chunk, ws.data_ptr(), n.value, None) == L.SA_OK
+    torch.cuda.synchronize()
+    assert cache.read_status() == L.SA_ERR_TIMEOUT
+    # the line of units, cut evenly: what each CTA holds from that chunk on (wait 8: if a part ends with it)
+    base, rem = divmod(2 * T * ch, n_cta)
+    ends = [base * i + min(i, rem) for i in range(n_cta + 1)]
+    lost = np.zeros(2 * T, bool)
+    for w0, w1 in zip(ends, ends[1:]):
+        at = w0 + chunk
+        if at < w1 and (wait < 8 or at % ch == ch - 1 or at == w1 - 1):
+            lost[[w // ch for w in range(at, w1)]] = True
+    assert lost.any() and (chunk < 2) >= lost.all()        # from chunk 2 on, some units come before
+    lost = torch.from_numpy(lost).view(T, 2).repeat_interleave(64, 1).cuda()
+    assert bool((torch.isnan(o2) == lost[..., None]).all()) and bool((torch.isnan(lse2) == lost).all())
+    assert bool((o2[~lost] == o[~lost]).all()) and bool((lse2[~lost] == lse[~lost]).all())
 
 
 @pytest.mark.parametrize("B", [0, 2])

@@ -172,6 +172,16 @@ def test_a_step_without_tokens_or_requests_asks_for_nothing():
     assert r.returncode == 0, (r.returncode, r.stdout[-200:], r.stderr[-500:])
 
 
+@pytest.mark.parametrize("args,kw,status", [
+    ((9, 0, 0), {}, L.SA_ERR_PARAM), ((8, 3, 0), {}, L.SA_ERR_PARAM), ((7, 2, 0), {}, L.SA_ERR_PARAM),
+    ((0, 9, 0), {}, L.SA_ERR_PARAM), ((8, 0, -1), {}, L.SA_ERR_PARAM), ((8, 0, 0), dict(t_q=-1), L.SA_ERR_PARAM),
+    ((8, 0, 0), dict(t_q=0), L.SA_ERR_UNSUPPORTED),
+])
+def test_bad_give_up_checks_are_refused(args, kw, status):
+    c, q = _cache(kv_shared=1, d_qk=576, d_v=512, n_heads_kv=1, **kw), _query(n_heads_q=64, q_stride=64 * 576)
+    assert L.lib().sa_selftest_kv8_give_up(ctypes.byref(c), ctypes.byref(q), *args, FAKE, 1 << 40, None) == status
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=5), L.SA_ERR_PARAM), (dict(k=None), L.SA_ERR_NULLPTR), (dict(v=None), L.SA_ERR_NULLPTR),
     (dict(k_stride=248), L.SA_ERR_PARAM), (dict(v_stride=260), L.SA_ERR_PARAM), (dict(k=FAKE + 4), L.SA_ERR_PARAM),

@@ -156,7 +156,7 @@ EXPORTS = ["sa_fwd_get_workspace_size", "sa_fwd", "sa_bwd_get_workspace_size", "
            "sa_selftest_mma2", "sa_plan", "sa_read_status", "sa_bwd_no_alloc_read_status",
            "sa_debug_block_index", "sa_selftest_gather4", "sa_softmax_l1norm",
            "sa_indexer_kl_grad_get_workspace_size", "sa_indexer_kl_grad", "sa_page_plan", "sa_kv8_write",
-           "sa_kv8_fwd_get_workspace_size", "sa_kv8_fwd"]
+           "sa_kv8_fwd_get_workspace_size", "sa_kv8_fwd", "sa_selftest_kv8_give_up"]
 
 
 def lib() -> ctypes.CDLL:
@@ -180,6 +180,8 @@ def lib() -> ctypes.CDLL:
         L.sa_kv8_write.argtypes = [P(SaKv8Cache), P(SaKv8Rows), _vp]
         L.sa_kv8_fwd_get_workspace_size.argtypes = [P(SaKv8Cache), P(SaKv8Query), P(ctypes.c_size_t)]
         L.sa_kv8_fwd.argtypes = [P(SaKv8Cache), P(SaKv8Query), _vp, ctypes.c_size_t, _vp]
+        L.sa_selftest_kv8_give_up.argtypes = [P(SaKv8Cache), P(SaKv8Query)] + [ctypes.c_int32] * 3 + [
+            _vp, ctypes.c_size_t, _vp]
         L.sa_debug_resolve.argtypes = [P(SaArgs), _vp, _vp, ctypes.c_int32, _vp]
         L.sa_status_string.argtypes = [ctypes.c_int32]
         L.sa_status_string.restype = ctypes.c_char_p

@@ -67,6 +67,7 @@ struct K8Fwd {
   const float* sinks;
   void* o;
   float* lse;
+  int give_up_warp, give_up_wait, give_up_chunk;  // launch_kv8_give_up
 };
 
 struct PagePlan {
@@ -83,5 +84,7 @@ cudaError_t launch_kv8_write(K8Write a, cudaStream_t st);
 bool k8_built(int dqk, int dv, bool shared);
 size_t k8_fwd_workspace(K8Fwd a);
 cudaError_t launch_kv8_fwd(K8Fwd a, void* ws, cudaStream_t st);
+// The tcgen05 kernel with one wait counted as given up; cudaErrorNotSupported where another kernel runs.
+cudaError_t launch_kv8_give_up(K8Fwd a, void* ws, cudaStream_t st);
 
 }  // namespace sa

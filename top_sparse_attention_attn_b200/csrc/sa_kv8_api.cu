@@ -190,4 +190,20 @@ sa_status sa_kv8_fwd(const sa_kv8_cache* cache, const sa_kv8_query* query, void*
   return cuda_status(sa::launch_kv8_fwd(a, ws, static_cast<cudaStream_t>(stream)));
 }
 
+sa_status sa_selftest_kv8_give_up(const sa_kv8_cache* cache, const sa_kv8_query* query, int32_t warp, int32_t wait,
+                                  int32_t chunk, void* ws, size_t ws_bytes, void* stream) {
+  sa_status st = validate_query(cache, query);
+  if (st != SA_OK) return st;
+  if (warp < 0 || warp > 8 || wait < 0 || wait > 8 || (warp == 8) != (wait < 3) || chunk < 0) return SA_ERR_PARAM;
+  sa::K8Fwd a = make_fwd(cache, query);
+  const size_t need = sa::k8_fwd_workspace(a);
+  if (need && (!ws || ws_bytes < need)) return SA_ERR_WORKSPACE;
+  if (need && !aligned16(ws)) return SA_ERR_PARAM;
+  a.give_up_warp = warp;
+  a.give_up_wait = wait;
+  a.give_up_chunk = chunk;
+  const cudaError_t e = sa::launch_kv8_give_up(a, ws, static_cast<cudaStream_t>(stream));
+  return e == cudaErrorNotSupported ? SA_ERR_UNSUPPORTED : cuda_status(e);
+}
+
 }  // extern "C"

@@ -1551,16 +1551,29 @@ __device__ __forceinline__ K8Codes tc_ld32(const uint8_t* p) {  // 32 codes, 32-
   }
   return r;
 }
-template <int FMT>
+// GIVE_UP, for the test of what a wait that gave up leaves behind: a wait of one warp at one chunk completes and
+// counts as given up; all others are made as ever, so that nothing runs out of turn.
+template <int FMT, bool GIVE_UP>
 __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K8Fwd a, float* ws) {
   using P = K8Tc;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023);
   __shared__ K8Found found;
   __shared__ uint32_t tmem_at;
-  __shared__ int abort_word, fresh;  // fresh: the chunk begins a part, O^T is overwritten
+  // abort_word: a wait of this CTA gave up.  Whichever warp it was (the one that issues goes on with operands that
+  // are not all there, and what it commits lets the others' waits complete), the unit at hand and the share's
+  // later ones become NaN.  fresh: the chunk begins a part, O^T is overwritten.
+  __shared__ int abort_word, fresh;
   const K8Cache& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto wait = [&](int which, long long chunk, uint64_t* bar, uint32_t parity) -> bool {
+    if (!GIVE_UP) return mbar_wait(bar, parity, &abort_word, c.status);
+    mbar_wait_drain(bar, parity);
+    if (warp != a.give_up_warp || which != a.give_up_wait || chunk != a.give_up_chunk) return true;
+    abort_word = 1;
+    if (c.status) atomicOr(c.status, kStatusTimeout);
+    return false;
+  };
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + P::kBarAt);
   uint64_t *const p_full = full + 2, *const s_done = full + 3, *const blk_free = full + 4, *const drained = full + 8;
   if (tid == 0) {
@@ -1593,8 +1606,8 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
       const uint32_t dv = (uint32_t)sdesc(kat, kTcSlab, 1024), dp = (uint32_t)sdesc(pat, kTcSlab, 1024);
       const uint32_t hi = (uint32_t)(sdesc(0, 0, 1024) >> 32);
       constexpr uint32_t id_s = k8_idesc(128, 64, false, false), id_o = k8_idesc(128, 64, true, true);
-      // A wait that gave up changes nothing here (the later ones return at once, the products are not used):
-      // the warp stays together, as electing asks for.
+      // A wait that gave up changes nothing here (abort_word keeps the products out of the result): the warp stays
+      // together, as electing asks for.
       for (long long n = 0; n < n_chunks; ++n) {
         const uint32_t ph = (uint32_t)(n & 1);
         // Unrolled with constant offsets from bases that the compiler sees to be alike in the whole warp, so that
@@ -1603,7 +1616,7 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
 #pragma unroll
         for (int sl = 0; sl < kTcSlabs; ++sl) {
           if ((sl & 3) == 0 && sl < 8) {  // four slabs, then five: a wait and its fence cost 300 to 500 cycles
-            mbar_wait(full + (sl >> 2), ph, &abort_word, c.status);
+            wait(sl >> 2, n, full + (sl >> 2), ph);
             fence_async_smem();  // the converting warps' stores, seen through the barrier, before the MMAs' reads
             tc_fence_after();
           }
@@ -1615,7 +1628,7 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
             if (sl == kTcSlabs - 1) mma_commit(s_done);
           }
         }
-        mbar_wait(p_full, ph, &abort_word, c.status);
+        wait(2, n, p_full, ph);
         fence_async_smem();
         tc_fence_after();
         const uint32_t over = *(volatile int*)&fresh;
@@ -1788,7 +1801,7 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
         };
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          if (n > 0 && !dead) dead = !mbar_wait(blk_free + g, ph ^ 1, &abort_word, c.status);
+          if (n > 0 && (GIVE_UP || !dead)) dead |= !wait(3 + g, n, blk_free + g, ph ^ 1);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             put(raw[2 * g + j], 2 * g + ((lane >> 1) & 1), warp * 16 + 8 * j + (lane >> 2), 4 * (lane & 1), lane & 2);
@@ -1814,7 +1827,7 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
         // --- softmax: this thread's row against 32 heads ---
         const bool see = see_of[ph * kTcRows + row_j] != 0;
         const float ks = k8_scale(scale_of[ph * kTcRows + row_j]), lv = k8_log2(ks), iv = k8_rcp(ks);
-        if (!dead) dead = !mbar_wait(s_done, ph, &abort_word, c.status);
+        if (GIVE_UP || !dead) dead |= !wait(7, n, s_done, ph);
         tc_fence_after();
         float s[32];
         {
@@ -1907,7 +1920,7 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
       }
 
       // --- the part's sums, and O^T out ---
-      if (!dead) dead = !mbar_wait(blk_free + 3, (uint32_t)((n - 1) & 1), &abort_word, c.status);
+      if (GIVE_UP || !dead) dead |= !wait(8, n - 1, blk_free + 3, (uint32_t)((n - 1) & 1));
       tc_fence_after();
 #pragma unroll
       for (int d = 16; d; d >>= 1)
@@ -1917,14 +1930,14 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
           l[i] = keep + __shfl_xor_sync(~0u, give, d);
         }
       red[(warp & 3) * 64 + 32 * hh + lane] = l[0];  // lane x holds head x's
-      tc_bar();
+      const bool lost = tc_any(*(volatile int*)&abort_word != 0);
       const bool whole = u.c0 == 0 && u.c1 == u.ch;
       float* const part_out = k8_part(ws, gridDim.x, 2 * blockIdx.x + (u.c0 == 0), 64, kLatDV);
       float norm = 0.f;
       if (tid < u.rows) {
         const float m = first ? -INFINITY : head_of[tid].y + kK8Top;
         const float total =
-            dead ? __int_as_float(0x7fffffff) : red[tid] + red[64 + tid] + red[128 + tid] + red[192 + tid];
+            lost ? __int_as_float(0x7fffffff) : red[tid] + red[64 + tid] + red[128 + tid] + red[192 + tid];
         if (whole) {
           float lse;
           norm = k8_norm(k8_sink(a, u.head0 + tid), m, total, &lse);
@@ -1996,19 +2009,24 @@ static cudaError_t latent_t(const K8Fwd& a, void* ws, cudaStream_t st) {
   count_launch();
   return launch_pdl(k8_join_kernel<MT * 16, kLatDV>, (unsigned)n, 256, 0, st, a, static_cast<float*>(ws), n);
 }
+template <int FMT, bool GIVE_UP>
+static cudaError_t tc_t(const K8Fwd& a, void* ws, cudaStream_t st) {
+  auto k = k8_tc_kernel<FMT, GIVE_UP>;
+  static unsigned long long done = 0;
+  cudaError_t e = allow_smem(k, K8Tc::kSmem, done);
+  if (e != cudaSuccess) return e;
+  const int n = k8_ctas(a);
+  count_launch();
+  e = launch_pdl(k, (unsigned)n, 384, K8Tc::kSmem, st, a, static_cast<float*>(ws));
+  if (e != cudaSuccess || n == 1 || a.per_unit == 1) return e;
+  count_launch();
+  return launch_pdl(k8_join_kernel<64, kLatDV>, (unsigned)n, 256, 0, st, a, static_cast<float*>(ws), n);
+}
 template <int FMT>
 static cudaError_t latent_f(const K8Fwd& a, void* ws, cudaStream_t st) {
   if (a.unit_rows == 16) return latent_t<1, FMT>(a, ws, st);
   if (a.unit_rows == 32) return latent_t<2, FMT>(a, ws, st);
-  static unsigned long long done = 0;
-  cudaError_t e = allow_smem(k8_tc_kernel<FMT>, K8Tc::kSmem, done);
-  if (e != cudaSuccess) return e;
-  const int n = k8_ctas(a);
-  count_launch();
-  e = launch_pdl(k8_tc_kernel<FMT>, (unsigned)n, 384, K8Tc::kSmem, st, a, static_cast<float*>(ws));
-  if (e != cudaSuccess || n == 1 || a.per_unit == 1) return e;
-  count_launch();
-  return launch_pdl(k8_join_kernel<64, kLatDV>, (unsigned)n, 256, 0, st, a, static_cast<float*>(ws), n);
+  return tc_t<FMT, false>(a, ws, st);
 }
 
 static void k8_geometry(K8Fwd& a) {
@@ -2054,6 +2072,12 @@ cudaError_t launch_kv8_fwd(K8Fwd a, void* ws, cudaStream_t st) {
   if (a.c.dqk == 64) return split_d<64, 64>(a, ws, st);
   if (a.c.dqk == 128) return split_d<128, 128>(a, ws, st);
   return split_d<192, 128>(a, ws, st);
+}
+
+cudaError_t launch_kv8_give_up(K8Fwd a, void* ws, cudaStream_t st) {
+  if (a.c.T == 0 || a.c.B == 0 || !k8_latent(a) || a.c.fmt != kFmtE4M3) return cudaErrorNotSupported;
+  k8_geometry(a);
+  return a.unit_rows == 64 ? tc_t<kFmtE4M3, true>(a, ws, st) : cudaErrorNotSupported;
 }
 
 }  // namespace sa
