@@ -3,6 +3,7 @@ against independent computations, and the refusals of the C ABI and of the wrapp
 
 import ctypes
 import os
+import re
 import subprocess
 import sys
 
@@ -211,6 +212,19 @@ def test_bad_plans_are_refused(kw, status):
     for k, v in kw.items():
         setattr(a, k, v)
     assert L.lib().sa_page_plan(ctypes.byref(a), None) == status
+
+
+def test_kernels_that_start_early_read_with_ordinary_loads():
+    """The kernels begin behind a programmatic dependency, so that what they read may have been written while they
+    lived: no load through the read-only path, nor a pointer that lets the compiler choose it."""
+    csrc = os.path.join(ROOT, "top_sparse_attention_attn_b200", "csrc")
+    files = [f for f in os.listdir(csrc) if f.startswith("sa_kv8")]
+    assert len(files) == 5
+    for f in files:
+        with open(os.path.join(csrc, f)) as src:
+            code = re.sub(r"//[^\n]*|/\*.*?\*/", "", src.read(), flags=re.S)
+        for word in ("__ldg", ".nc", "__restrict__"):
+            assert word not in code, (f, word)
 
 
 # ---- refusals: the wrapper ------------------------------------------------------

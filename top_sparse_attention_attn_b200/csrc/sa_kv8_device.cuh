@@ -14,6 +14,13 @@ namespace sa {
 __device__ __forceinline__ int k8_quot(const K8Div& v, int n) { return (int)(__umulhi(2u * (uint32_t)n, v.m) >> v.s); }
 __device__ __forceinline__ int k8_rem(const K8Div& v, int n) { return n - k8_quot(v, n) * v.d; }
 
+// Every read of the caller's memory is an ordinary load (or a copy): the kernels start while the call before them
+// still writes, and the non-coherent loads are only for what nothing writes as long as a kernel lives.
+template <typename T>
+__device__ __forceinline__ T k8_read(const T* p) {
+  return *p;
+}
+
 // Scales as the kernels use them: [2^-60, 2^60], NaN as 2^-60 (fmaxf drops it).
 __device__ __forceinline__ float k8_scale(float s) { return fminf(fmaxf(s, 0x1p-60f), 0x1p60f); }
 
@@ -22,10 +29,10 @@ struct K8Seq {
   int t0, n, L, first;
 };
 __device__ __forceinline__ int k8_cu(const K8Cache& c, int b) {
-  return c.cu ? min(max(__ldg(c.cu + b), 0), c.T) : b * c.s_q;
+  return c.cu ? min(max(k8_read(c.cu + b), 0), c.T) : b * c.s_q;
 }
 __device__ __forceinline__ int k8_len(const K8Cache& c, int b) {
-  return min(max(__ldg(c.lens + b), 0), c.max_pages * c.ps);
+  return min(max(k8_read(c.lens + b), 0), c.max_pages * c.ps);
 }
 __device__ __forceinline__ K8Seq k8_seq(const K8Cache& c, int b) {
   K8Seq s;

@@ -212,7 +212,7 @@ struct K8Share {
 
 // sink: a head's sink logit times log2(e), -inf for none.
 __device__ __forceinline__ float k8_sink(const K8Fwd& a, int head) {
-  return a.sinks ? __ldg(a.sinks + head) * 1.4426950408889634f : -INFINITY;
+  return a.sinks ? k8_read(a.sinks + head) * 1.4426950408889634f : -INFINITY;
 }
 // What an output row's O is multiplied by, from its maximum, sum and sink; and its lse.
 __device__ __forceinline__ float k8_norm(float sink, float m, float l, float* lse) {
@@ -421,7 +421,7 @@ __device__ __forceinline__ K8Unit k8_take(const K8Fwd& a, K8Cursor& cur) {
   const long long iu = (long long)u.t0 * a.c.Hkv + u.h;
   u.idx = a.topk ? a.idx + iu * a.topk : nullptr;
   u.slots = a.topk;
-  if (a.topk && a.topk_len) u.slots = min(u.slots, max(0, __ldg(a.topk_len + iu)));
+  if (a.topk && a.topk_len) u.slots = min(u.slots, max(0, k8_read(a.topk_len + iu)));
   u.table = a.c.table + cur.b * a.c.tstride;
   cur.w0 += u.c1 - u.c0 + (u.c0 ? 0 : a.over);
   k8_next(cur);
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
     if (!a.topk || un < 0) return 0;
     const K8Unit& u = units[un];
     const int slot = k8_quot(a.by_bs, (u.c0 + k) * kK8Chunk + lane_row);
-    return slot < u.slots ? __ldg(u.idx + slot) : -1;
+    return slot < u.slots ? k8_read(u.idx + slot) : -1;
   };
   auto resolve = [&](int un, int k, int x) -> int {  // its (first) row, -1: none
     if (un < 0) return -1;
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
     const int last = ROWS ? row : row + 15;
     return row < u.hi && last >= u.lo ? row : -1;
   };
-  auto fetch_page = [&](int un, int row) -> int { return row >= 0 ? __ldg(units[un].table + k8_quot(c.by_ps, row)) : 0; };
+  auto fetch_page = [&](int un, int row) -> int { return row >= 0 ? k8_read(units[un].table + k8_quot(c.by_ps, row)) : 0; };
   int fx = 0, f_row = -1, f_page = 0, f_head = 0;
   // the page of the step that the fetch stands at, then the index of the one behind it
   auto look = [&]() {
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
                       ((long long)(u.t0 + tok) * a.qstride + (long long)(u.head0 + qrow - tok * a.gdiv) * DK) * 2;
 #pragma unroll
     for (int i = 0; i < kQw; ++i)
-      raw[i] = qrow < u.rows ? __ldg(reinterpret_cast<const uint4*>(src + (qp + 8 * i) * 16)) : make_uint4(0, 0, 0, 0);
+      raw[i] = qrow < u.rows ? k8_read(reinterpret_cast<const uint4*>(src + (qp + 8 * i) * 16)) : make_uint4(0, 0, 0, 0);
   };
   auto lay_q = [&]() {
     // halves times 2^(14 - E), E the exponent of the row's largest, in the MMA's order
@@ -1137,7 +1137,7 @@ __global__ void __launch_bounds__(256, 1) k8_latent_kernel(const __grid_constant
     const long long iu = (long long)t * c.Hkv + h;
     const int* idx = a.topk ? a.idx + iu * a.topk : nullptr;
     int slots = a.topk;
-    if (a.topk && a.topk_len) slots = min(slots, max(0, __ldg(a.topk_len + iu)));
+    if (a.topk && a.topk_len) slots = min(slots, max(0, k8_read(a.topk_len + iu)));
     const int* table = c.table + b * c.tstride;
 
     // warp w resolves and copies rows 8 w .. 8 w + 7 of a chunk (lane x: row x % 8)
@@ -1145,7 +1145,7 @@ __global__ void __launch_bounds__(256, 1) k8_latent_kernel(const __grid_constant
     auto fetch_idx = [&](int k) -> int {
       if (!a.topk) return 0;
       const int slot = k8_quot(a.by_bs, p0 + k * kLatRows);
-      return k < n_steps && slot < slots ? __ldg(idx + slot) : -1;
+      return k < n_steps && slot < slots ? k8_read(idx + slot) : -1;
     };
     auto resolve = [&](int k, int x) -> int {
       if (k >= n_steps) return -1;
@@ -1161,7 +1161,7 @@ __global__ void __launch_bounds__(256, 1) k8_latent_kernel(const __grid_constant
       }
       return row < hi && row >= lo ? row : -1;
     };
-    auto fetch_page = [&](int row) -> int { return row >= 0 ? __ldg(table + k8_quot(c.by_ps, row)) : 0; };
+    auto fetch_page = [&](int row) -> int { return row >= 0 ? k8_read(table + k8_quot(c.by_ps, row)) : 0; };
     auto issue = [&](int st, int row, int page) {
       if (row >= 0 && (page < 0 || page >= c.n_pages)) {
         if (c.status) atomicOr(c.status, kStatusIndexRange);
@@ -1206,7 +1206,7 @@ __global__ void __launch_bounds__(256, 1) k8_latent_kernel(const __grid_constant
       uint4 raw[9];
 #pragma unroll
       for (int i = 0; i < 9; ++i)
-        raw[i] = row < rows ? __ldg(reinterpret_cast<const uint4*>(src + (qp + 8 * i) * 16)) : make_uint4(0, 0, 0, 0);
+        raw[i] = row < rows ? k8_read(reinterpret_cast<const uint4*>(src + (qp + 8 * i) * 16)) : make_uint4(0, 0, 0, 0);
       float big = 0.f;
 #pragma unroll
       for (int i = 0; i < 9; ++i) {
@@ -1541,7 +1541,7 @@ __device__ __forceinline__ bool tc_elect() {
 __device__ __forceinline__ K8Codes tc_ld32(const uint8_t* p) {  // 32 codes, 32-byte aligned; none: zeros
   K8Codes r;
   if (p) {
-    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
                  : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
                    "=r"(r.w[7])
                  : "l"(p));
@@ -1666,7 +1666,7 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
       auto fetch_idx = [&](int k) -> int {
         if (!a.topk) return 0;
         const int slot = k8_quot(a.by_bs, p0 + k * kTcRows);
-        return k < n_steps && slot < u.slots ? __ldg(u.idx + slot) : -1;
+        return k < n_steps && slot < u.slots ? k8_read(u.idx + slot) : -1;
       };
       auto resolve = [&](int k, int x) -> int {
         if (k >= n_steps) return -1;
@@ -1682,7 +1682,7 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
         }
         return row < u.hi && row >= u.lo ? row : -1;
       };
-      auto fetch_page = [&](int row) -> int { return row >= 0 ? __ldg(u.table + k8_quot(c.by_ps, row)) : 0; };
+      auto fetch_page = [&](int row) -> int { return row >= 0 ? k8_read(u.table + k8_quot(c.by_ps, row)) : 0; };
       // the lane's row of the cache, from what was looked up (-1: none), and its scale
       float ks_next = 0.f;
       auto place = [&](int row, int page) -> int {
@@ -1691,7 +1691,7 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
           row = -1;
         }
         if (row < 0) return -1;
-        ks_next = __ldg(c.ks + (long long)page * c.Hkv + u.h);
+        ks_next = k8_read(c.ks + (long long)page * c.Hkv + u.h);
         return page * c.ps + k8_rem(c.by_ps, row);
       };
       auto note = [&](uint32_t ph, int rr) {  // for the softmax
@@ -1729,7 +1729,7 @@ __global__ void __launch_bounds__(384, 1) k8_tc_kernel(const __grid_constant__ K
         const char* src = static_cast<const char*>(a.q) + ((long long)u.t0 * a.qstride + (long long)(u.head0 + row) * kLatDK) * 2;
 #pragma unroll
         for (int i = 0; i < 9; ++i)
-          qr[y][i] = row < u.rows ? __ldg(reinterpret_cast<const uint4*>(src + ((lane & 7) + 8 * i) * 16)) : make_uint4(0, 0, 0, 0);
+          qr[y][i] = row < u.rows ? k8_read(reinterpret_cast<const uint4*>(src + ((lane & 7) + 8 * i) * 16)) : make_uint4(0, 0, 0, 0);
       }
       const int row0 = resolve(0, x0), pg0 = fetch_page(row0), row1 = resolve(1, x1), pg1 = fetch_page(row1);
       int next_row = resolve(2, x2), next_page = fetch_page(next_row);

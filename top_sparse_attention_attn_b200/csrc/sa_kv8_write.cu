@@ -34,13 +34,13 @@ __global__ void page_plan_kernel(PagePlan p) {
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  const int n_free = min(max(__ldg(p.n_free), 0), p.free_cap);
+  const int n_free = min(max(k8_read(p.n_free), 0), p.free_cap);
   if (tid == 0) fail = p.B;
   const int per = (p.B + nt - 1) / nt, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   // sums of this thread's requests (64 bits: the lengths are the caller's)
   long long tok = 0, page = 0;
   for (int b = b0; b < b1; ++b) {
-    const long long o = __ldg(p.old_lens + b), n = __ldg(p.new_lens + b);
+    const long long o = k8_read(p.old_lens + b), n = k8_read(p.new_lens + b);
     if (o < 0 || n < 0) continue;
     tok += n;
     page += (o + n + p.ps - 1) / p.ps - (o + p.ps - 1) / p.ps;
@@ -67,7 +67,7 @@ __global__ void page_plan_kernel(PagePlan p) {
   long long ct = it - tok + (warp ? wtok[warp - 1] : 0), cp = ip - page + (warp ? wpage[warp - 1] : 0);
   int bad = p.B;
   for (int b = b0; b < b1; ++b) {
-    const long long o = __ldg(p.old_lens + b), n = __ldg(p.new_lens + b);
+    const long long o = k8_read(p.old_lens + b), n = k8_read(p.new_lens + b);
     // sums behind the first request that fails are never used; they only need to stay in range
     cu[b] = (int)min(ct, (long long)p.T);
     pg[b] = (int)min(cp, (long long)n_free);
@@ -89,7 +89,7 @@ __global__ void page_plan_kernel(PagePlan p) {
   const int n_tok = cu[served], n_new = pg[served];
   if (blockIdx.x == 0) {
     for (int b = tid; b <= p.B; b += nt) p.cu[b] = b < served ? cu[b] : n_tok;
-    for (int b = tid; b < p.B; b += nt) p.seq_lens[b] = __ldg(p.old_lens + b) + (b < served ? __ldg(p.new_lens + b) : 0);
+    for (int b = tid; b < p.B; b += nt) p.seq_lens[b] = k8_read(p.old_lens + b) + (b < served ? k8_read(p.new_lens + b) : 0);
     if (tid == 0) {
       *p.n_free_out = n_free - n_new;
       *p.n_served = served;
@@ -98,17 +98,17 @@ __global__ void page_plan_kernel(PagePlan p) {
   const int gid = blockIdx.x * nt + tid, gn = gridDim.x * nt;
   for (int i = gid; i < n_new; i += gn) {
     const int b = plan_upper(pg, served, i);
-    const int held = (int)(((long long)__ldg(p.old_lens + b) + p.ps - 1) / p.ps);
-    p.table[b * p.tstride + held + i - pg[b]] = __ldg(p.free_pages + (n_free - 1 - i));
+    const int held = (int)(((long long)k8_read(p.old_lens + b) + p.ps - 1) / p.ps);
+    p.table[b * p.tstride + held + i - pg[b]] = k8_read(p.free_pages + (n_free - 1 - i));
   }
   for (int t = gid; t < p.T; t += gn) {
     long long slot = -1;
     if (t < n_tok) {
       const int b = plan_upper(cu, served, t);
-      const int o = __ldg(p.old_lens + b), pos = o + t - cu[b];
+      const int o = k8_read(p.old_lens + b), pos = o + t - cu[b];
       const int held = (int)(((long long)o + p.ps - 1) / p.ps), j = pos / p.ps;
       // entries below `held` are read here and entries from `held` on written above: never the same one
-      const int id = j < held ? p.table[b * p.tstride + j] : __ldg(p.free_pages + (n_free - 1 - (pg[b] + j - held)));
+      const int id = j < held ? p.table[b * p.tstride + j] : k8_read(p.free_pages + (n_free - 1 - (pg[b] + j - held)));
       if (id >= 0) slot = (long long)id * p.ps + (pos - j * p.ps);
     }
     p.slots[t] = slot;
@@ -185,7 +185,7 @@ __device__ __forceinline__ void k8_write_part(const char* x, long long stride, i
                                               const K8Cache& cc, const int* table, uint8_t* cache, float* scales, int h,
                                               int off, int tid, int bar, float* red) {
   constexpr int kHold = NT == 512 ? 9 : NT == 128 ? 12 : 4;  // 64 rows of 576 or of 192; a few rows
-  const int page = __ldg(table), fmt = cc.fmt;
+  const int page = k8_read(table), fmt = cc.fmt;
   const int per = d >> 3, n8 = m * per;
   auto piece = [&](int i, int& r, int& c) {
     r = k8_quot(by_per, i);
@@ -197,7 +197,7 @@ __device__ __forceinline__ void k8_write_part(const char* x, long long stride, i
     const int i = tid + j * NT;
     int r, c;
     piece(i, r, c);
-    if (i < n8) hold[j] = __ldg(reinterpret_cast<const uint4*>(x + r * stride * 2 + c * 16));
+    if (i < n8) hold[j] = k8_read(reinterpret_cast<const uint4*>(x + r * stride * 2 + c * 16));
   }
   if (page < 0 || page >= cc.n_pages) {
     if (cc.status) atomicOr(cc.status, kStatusIndexRange);
@@ -217,7 +217,7 @@ __device__ __forceinline__ void k8_write_part(const char* x, long long stride, i
     for (int i = tid + kHold * NT; i < n8; i += NT) {
       int r, c;
       piece(i, r, c);
-      most(__ldg(reinterpret_cast<const uint4*>(x + r * stride * 2 + c * 16)));
+      most(k8_read(reinterpret_cast<const uint4*>(x + r * stride * 2 + c * 16)));
     }
   };
   auto meet = [&]() {
@@ -292,7 +292,7 @@ __device__ __forceinline__ void k8_write_part(const char* x, long long stride, i
   for (int i = tid + kHold * NT; i < n8; i += NT) {
     int r, c;
     piece(i, r, c);
-    put(i, __ldg(reinterpret_cast<const uint4*>(x + r * stride * 2 + c * 16)));
+    put(i, k8_read(reinterpret_cast<const uint4*>(x + r * stride * 2 + c * 16)));
   }
   asm volatile("bar.sync %0, %1;\n" ::"r"(bar), "n"(NT) : "memory");  // red[] and the old scale have been read
   if (tid == 0) *scale = after;
@@ -304,7 +304,7 @@ __device__ __forceinline__ int k8_find_warp(const K8Cache& c, int t, int lane) {
   int lo = 0, n = c.B;
   while (n > 1) {
     const int step = (n + 31) >> 5, at = lane * step;
-    const int below = __popc(__ballot_sync(~0u, at < n && __ldg(c.cu + lo + at) <= t));
+    const int below = __popc(__ballot_sync(~0u, at < n && k8_read(c.cu + lo + at) <= t));
     const int k = max(below - 1, 0);
     lo += k * step;
     n = min(step, n - k * step);
