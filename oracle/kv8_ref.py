@@ -114,8 +114,8 @@ def write(x, codes, scale, table, lens, cu, fmt):
                 a = np.where(np.isfinite(part), np.abs(part), 0.0).max()
                 s = scale_for(a, fmt)
                 if off:
-                    before = np.float64(scale[p, h])
-                    s = max(s, power_at_least(before if before > 0 else 0.0))
+                    before = read_scale(np.float64(scale[p, h]))
+                    s = max(s, power_at_least(before))
                     if s != before:
                         codes[p, :off, h] = round_codes(values(codes[p, :off, h], fmt) * (before / s), fmt)
                 codes[p, [r for r, _ in rows], h] = round_codes(part / s, fmt)

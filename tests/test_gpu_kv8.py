@@ -606,6 +606,26 @@ def test_a_step_served_in_two_slices():
     assert int(p.n_served) == B and torch.equal(o, o2) and torch.equal(lse, lse2) and lse.all()
 
 
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("n", [2, 12])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_write_behind_rows_with_any_scale(fmt, n, shared):
+    """Scales that no write leaves: the earlier rows are rounded again from what the attention reads them as."""
+    rng = np.random.default_rng(26)
+    odd = [0.0, -1.0, float("nan"), float("inf"), float("-inf"), 2.0 ** -70, 2.0 ** 70, 3.0, 0.25]
+    H, (dqk, dv) = len(odd), (576, 512) if shared else (64, 64)
+    lens, new = [20 + n, 40 + n], [n, n]
+    c = dict(lens=lens, new=new, H=H, dqk=dqk, dv=dv, fmt=fmt, shared=shared)
+    cache, table, _, _ = make_cache(rng, lens, page=64, H=H, dqk=dqk, dv=dv, fmt=fmt, shared=shared)
+    for s in (cache.k_scale,) if shared else (cache.k_scale, cache.v_scale):
+        s[torch.from_numpy(table[:, 0]).cuda()] = torch.tensor(odd, device="cuda")
+    k, v = (torch.from_numpy(rng.standard_normal((2 * n, H, d))).to(torch.bfloat16) for d in (dqk, dv))
+    k[n:] = 0                                              # rows that need no scale
+    kd, vd, cu = k.cuda(), None if shared else v.cuda(), [0, n, 2 * n]
+    _check_write(c, cache, table, k, v, cu,
+                 lambda: cache.write(kd, vd, _i32(table), _i32(lens), cu_seqlens_q=_i32(cu)))
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_write_of_infinities_nan_and_extremes(fmt):
     rng = np.random.default_rng(22)

@@ -46,6 +46,20 @@ def test_scale_is_the_least_power_of_two_that_holds(fmt):
         assert a <= top * s and (s == 2.0 ** -60 or a > top * s / 2)
 
 
+@pytest.mark.parametrize("fmt", R.FORMATS)
+@pytest.mark.parametrize("scale", [0.0, -3.0, np.nan, np.inf, 2.0 ** -70, 2.0 ** 70, 2.0 ** -60, 3.0])
+def test_an_append_keeps_what_the_earlier_rows_are_read_as(scale, fmt):
+    rng = np.random.default_rng(3)
+    codes = R.round_codes(rng.standard_normal((1, 8, 1, 16)) * 40, fmt)
+    was = R.values(codes[0, :5], fmt) * R.read_scale(scale)
+    sc = np.array([[scale]])
+    R.write(np.zeros((1, 1, 16)), codes, sc, np.array([[0]]), [6], [0, 1], fmt)
+    now = R.values(codes[0, :5], fmt) * R.read_scale(sc[0, 0])
+    # 3.0 is raised to 4.0: half a step of a code, or half of e4m3's smallest
+    err = np.maximum(np.abs(was) * 2.0 ** -4, 2.0 ** -10 * sc[0, 0]) if fmt == "e4m3" else sc[0, 0] / 2
+    assert (np.abs(now - was) <= (err if scale == 3.0 else 0)).all() and (codes[0, 5] == 0).all()
+
+
 def test_plan_serves_a_prefix_and_takes_pages_off_the_stack():
     table = np.full((4, 3), -1)
     table[0, 0] = 9

@@ -138,12 +138,10 @@ __device__ __forceinline__ int k8_exp_for(float a, int fmt) {
   const int e = fmt == kFmtE4M3 ? E - (m <= 0x600000u ? 8 : 7) : E - (m <= 0x7e0000u ? 6 : 5);
   return min(max(e, -60), 60);
 }
-// e of the least power of two at or above a scale that is already there
+// e of the least power of two at or above a scale that is already there (in [2^-60, 2^60])
 __device__ __forceinline__ int k8_exp_at_least(float a) {
-  if (!(a > 0.f)) return -60;
   const uint32_t u = __float_as_uint(a);
-  const int e = (int)(u >> 23) - 127 + ((u & 0x7fffffu) ? 1 : 0);
-  return min(max(e, -60), 60);
+  return (int)(u >> 23) - 127 + ((u & 0x7fffffu) ? 1 : 0);
 }
 __device__ __forceinline__ float k8_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
@@ -206,7 +204,7 @@ __device__ __forceinline__ void k8_write_part(const char* x, long long stride, i
   float* const scale = scales + (long long)page * cc.Hkv + h;
   const long long row_bytes = (long long)cc.Hkv * d;
   uint8_t* const codes = cache + (long long)page * cc.ps * row_bytes + (long long)h * d;
-  const float before = off ? *scale : 0.f;
+  const float before = off ? k8_scale(*scale) : 0.f;  // as the attention reads it
   // The maximum, two elements at a time (NaN loses); once more, one by one, where it is infinite: infinities
   // and NaN set no scale.
   float a = 0.f;
