@@ -295,6 +295,21 @@ def test_wrapper_refuses_wrong_types_shapes_and_strides():
         c.write(k, k, **s)
 
 
+@pytest.mark.parametrize("shared", [False, True])
+def test_dequantize_reads_scales_as_the_attention_does(shared):
+    c = _cpu_cache(shared, fmt="int8")
+    odd = torch.tensor([[0.0, -1.0], [float("nan"), float("inf")], [-float("inf"), 2.0 ** -70], [2.0 ** 70, 3.0],
+                        [0.25, 2.0 ** 60], [1.0, 2.0 ** -60]])
+    for x, s in ((c.k, c.k_scale),) if shared else ((c.k, c.k_scale), (c.v, c.v_scale)):
+        x.copy_(torch.arange(x.numel()).remainder(255).sub(127).view(x.shape))
+        s.copy_(odd)
+    k, v = c.dequantize()
+    assert (v is None) == shared
+    for x, got in ((c.k, k),) if shared else ((c.k, k), (c.v, v)):
+        want = x.numpy().astype(np.float64) * R.read_scale(odd.numpy().astype(np.float64))[:, None, :, None]
+        assert np.array_equal(got.numpy(), want)
+
+
 def test_empty_tensors_may_have_any_strides():
     """Without elements a tensor is contiguous whatever its strides: the checks pass, up to the one for a GPU."""
     c = _cpu_cache()

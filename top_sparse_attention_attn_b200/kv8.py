@@ -146,6 +146,8 @@ class Kv8Cache:
             return L.sa_read_status(self.status.data_ptr(), 4, st)
 
     def dequantize(self):
-        """(k, v) as fp32 tensors of the cache's shape (v None for a shared row)."""
-        k = self.k.float() * self.k_scale[:, None, :, None]
-        return k, None if self.v is None else self.v.float() * self.v_scale[:, None, :, None]
+        """(k, v) as fp32 tensors of the cache's shape (v None for a shared row), as attend reads them."""
+        def values(codes, scale):
+            s = torch.where(scale.isnan(), 0.0, scale).clamp(2.0 ** -60, 2.0 ** 60)
+            return codes.float() * s[:, None, :, None]
+        return values(self.k, self.k_scale), None if self.v is None else values(self.v, self.v_scale)
