@@ -360,6 +360,28 @@ def test_bad_pages_and_indices_select_nothing_and_raise_the_bit():
     assert cache.read_status() == L.SA_ERR_INDEX
 
 
+@pytest.mark.parametrize("given", [None, 0, "side"])
+def test_the_status_word_is_sticky_until_it_is_cleared(given):
+    rng = np.random.default_rng(55)
+    lens, cu = [200, 120], [0, 1, 2]
+    cache, table, _, _ = make_cache(rng, lens, page=64, H=2, dqk=128, dv=128)
+    bad = table.copy()
+    bad[0, 1] = -1
+    q = torch.randn((2, 8, 128), device="cuda").to(torch.bfloat16)
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if given == "side" else given
+    args = [(q, _i32(t), _i32(lens)) for t in (table, bad)]
+    cu = _i32(cu)
+    torch.cuda.synchronize()
+    for clear in (False, True):
+        cache.attend(*args[1], cu_seqlens_q=cu, stream=stream)
+        if clear:
+            cache.clear_status(stream)
+        cache.attend(*args[0], cu_seqlens_q=cu, stream=stream)
+        assert cache.read_status(stream) == (L.SA_OK if clear else L.SA_ERR_INDEX)
+    torch.cuda.synchronize()
+
+
 def test_duplicate_indices_count_twice_and_topk_len_cuts():
     rng = np.random.default_rng(10)
     lens, cu = [300], [0, 2]

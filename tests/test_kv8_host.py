@@ -295,6 +295,13 @@ def test_wrapper_refuses_wrong_types_shapes_and_strides():
         c.write(k, k, **s)
 
 
+def test_the_status_word_can_be_cleared():
+    c = _cpu_cache()
+    c.status.fill_(3)
+    c.clear_status()
+    assert int(c.status) == 0
+
+
 @pytest.mark.parametrize("shared", [False, True])
 def test_dequantize_reads_scales_as_the_attention_does(shared):
     c = _cpu_cache(shared, fmt="int8")

@@ -140,10 +140,19 @@ class Kv8Cache:
         return _check(r, "sa_kv8_fwd")
 
     def read_status(self, stream=None) -> int:
-        """The calls' status word so far, as an sa_status (synchronises the stream)."""
+        """The calls' status word since it was last cleared, as an sa_status (synchronises the stream)."""
         with torch.cuda.device(self._index):
             st = torch.cuda.current_stream(self._index).cuda_stream if stream is None else stream
             return L.sa_read_status(self.status.data_ptr(), 4, st)
+
+    def clear_status(self, stream=None) -> None:
+        """Clear the status word, in the stream's order: what read_status reported is not reported again, and
+        the calls behind it no longer give up their waits for a time-out that was met before."""
+        if self._index < 0 or stream is None:
+            self.status.zero_()
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device)):
+                self.status.zero_()
 
     def dequantize(self):
         """(k, v) as fp32 tensors of the cache's shape (v None for a shared row), as attend reads them."""
