@@ -56,20 +56,41 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if force or _stale(obj, src):
             jobs.append([nvcc(), *ARCH, *FLAGS, "-c", src, "-o", obj])
 
+    torch = _torch()
+    ext_obj, ext_for = os.path.join(BUILD, "kv8_ext.o"), os.path.join(BUILD, "kv8_ext.torch")
+    ext_stale = torch and (force or _stale(ext_obj, EXT_SRC) or _text(ext_for) != torch.__version__)
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, len(jobs) + 1)) as ex:
-        ext_obj = os.path.join(BUILD, "kv8_ext.o")
-        ext_stale = force or _stale(ext_obj, EXT_SRC)
-        ext = ex.submit(_run, _ext_compile(ext_obj)) if ext_stale else None
+        ext = ex.submit(_run, _ext_compile(torch, ext_obj)) if ext_stale else None
         for out in ex.map(_run, jobs):
             if verbose and out.strip():
                 print(out)
+        if jobs or not os.path.exists(LIB):
+            _run([nvcc(), *ARCH, "-shared", "-o", LIB, *objs, "-lcudart"])
         if ext:
             ext.result()
-    if jobs or not os.path.exists(LIB):
-        _run([nvcc(), *ARCH, "-shared", "-o", LIB, *objs, "-lcudart"])
-    if ext_stale or not os.path.exists(EXT):
-        _run(_ext_link(ext_obj))
+    if torch and (ext_stale or not os.path.exists(EXT)):
+        _run(_ext_link(torch, ext_obj))
+        with open(ext_for, "w") as f:
+            f.write(torch.__version__)
+    if verbose and not torch:
+        print("no torch with CUDA here: _kv8_ext.so is not built")
     return LIB
+
+
+def _torch():
+    """The torch that the CPython module is built against, or None: the C library needs none."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return torch if torch.version.cuda else None
+
+
+def _text(path: str) -> str:
+    if not os.path.exists(path):
+        return ""
+    with open(path) as f:
+        return f.read()
 
 
 def _run(cmd):
@@ -79,8 +100,7 @@ def _run(cmd):
     return r.stdout + r.stderr
 
 
-def _ext_compile(obj: str) -> list:
-    import torch
+def _ext_compile(torch, obj: str) -> list:
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     return ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
@@ -88,11 +108,10 @@ def _ext_compile(obj: str) -> list:
             "-isystem", sysconfig.get_paths()["include"], "-c", EXT_SRC, "-o", obj]
 
 
-def _ext_link(obj: str) -> list:
-    import torch
+def _ext_link(torch, obj: str) -> list:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    return ["g++", "-shared", "-o", EXT, obj, "-L" + HERE, "-l:libsparse_attn.so", "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
-            "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+    return ["g++", "-shared", "-o", EXT, obj, "-L" + HERE, "-l:libsparse_attn.so", "-L" + lib, "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
 
 
 if __name__ == "__main__":
