@@ -484,9 +484,10 @@ typedef struct sa_kv8_rows {
  * or, when the page holds rows before the first new one, the larger of that and the
  * scale it has (as it is read, raised to a power of two); those rows' codes are then
  * rounded again to the new scale where it changed (e4m3: exact short of subnormals
- * where the ratio is a power of two; integers lose the bits that the scale grew by).  A code is x / s rounded to nearest even and saturated;
- * NaN becomes the e4m3 NaN, or 0 in integers.  Two sequences must not write rows of
- * one page in the same call (the page's result is then undefined).
+ * where the ratio is a power of two; integers lose the bits that the scale grew by).
+ * A code is x / s rounded to nearest even and saturated; NaN becomes the e4m3 NaN,
+ * or 0 in integers.  Two sequences must not write rows of one page in the same call
+ * (the page's result is then undefined).  page_size * d_qk must not exceed 2^33.
  * Errors: SA_ERR_NULLPTR, SA_ERR_PARAM, SA_ERR_UNSUPPORTED (head sizes not built).
  * One kernel, no workspace.  Asynchronous. */
 sa_status sa_kv8_write(const sa_kv8_cache* cache, const sa_kv8_rows* rows, void* stream);

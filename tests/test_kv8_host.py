@@ -208,6 +208,16 @@ def test_bad_rows_are_refused(kw, status):
     assert L.lib().sa_kv8_write(ctypes.byref(_cache()), ctypes.byref(r), None) == status
 
 
+@pytest.mark.parametrize("kw", [dict(page_size=1 << 25, n_pages=3), dict(page_size=(1 << 30) // 72 + 1, n_pages=1)])
+def test_pages_of_more_pieces_than_32_bits_count_are_not_written(kw):
+    """33 M rows of 576 are 2.4e9 pieces of 8: counted in 32 bits, none of them would be written."""
+    r = L.SaKv8Rows(dtype=0, k=FAKE, k_stride=576)
+    c = _cache(kv_shared=1, d_qk=576, d_v=512, n_heads_kv=1, max_pages=1, **kw)
+    assert L.lib().sa_kv8_write(ctypes.byref(c), ctypes.byref(r), None) == L.SA_ERR_PARAM
+    c.page_size, c.t_q = (1 << 30) // 72, 0                # the largest that is taken, and nothing to launch
+    assert L.lib().sa_kv8_write(ctypes.byref(c), ctypes.byref(r), None) == L.SA_OK
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(batch=-1), L.SA_ERR_PARAM), (dict(batch=24577), L.SA_ERR_PARAM), (dict(page_size=0), L.SA_ERR_PARAM),
     (dict(max_pages=0), L.SA_ERR_PARAM), (dict(n_tokens=-1), L.SA_ERR_PARAM), (dict(table_stride=3), L.SA_ERR_PARAM),

@@ -155,6 +155,8 @@ sa_status sa_kv8_write(const sa_kv8_cache* cache, const sa_kv8_rows* rows, void*
   if (!rows) return SA_ERR_NULLPTR;
   if (rows->dtype != SA_DTYPE_BF16 && rows->dtype != SA_DTYPE_FP16) return SA_ERR_PARAM;
   const bool sep = !cache->kv_shared;
+  // a page's rows of a head are counted in 32 bits, by pieces of 8 elements (d_v is at most d_qk in every built pair)
+  if ((long long)cache->page_size * (cache->d_qk / 8) > (1ll << 30)) return SA_ERR_PARAM;
   if (rows->k_stride < (long long)cache->n_heads_kv * cache->d_qk || rows->k_stride % 8) return SA_ERR_PARAM;
   if (sep && (rows->v_stride < (long long)cache->n_heads_kv * cache->d_v || rows->v_stride % 8)) return SA_ERR_PARAM;
   if (tokens_of(cache) == 0 || cache->batch == 0) return SA_OK;
