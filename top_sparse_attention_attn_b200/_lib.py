@@ -292,25 +292,6 @@ def sa_softmax_l1norm(args: SaArgs, lse: int, ori_out, cmp_out, stream: int = 0)
     _check(lib().sa_softmax_l1norm(ctypes.byref(args), lse, ori_out, cmp_out, stream), "sa_softmax_l1norm")
 
 
-def sa_page_plan(args: SaPagePlanArgs, stream: int = 0) -> None:
-    _check(lib().sa_page_plan(ctypes.byref(args), stream), "sa_page_plan")
-
-
-def sa_kv8_write(cache: SaKv8Cache, rows: SaKv8Rows, stream: int = 0) -> None:
-    _check(lib().sa_kv8_write(ctypes.byref(cache), ctypes.byref(rows), stream), "sa_kv8_write")
-
-
-def sa_kv8_fwd_get_workspace_size(cache: SaKv8Cache, query: SaKv8Query) -> int:
-    n = ctypes.c_size_t(0)
-    _check(lib().sa_kv8_fwd_get_workspace_size(ctypes.byref(cache), ctypes.byref(query), ctypes.byref(n)),
-           "sa_kv8_fwd_get_workspace_size")
-    return n.value
-
-
-def sa_kv8_fwd(cache: SaKv8Cache, query: SaKv8Query, ws, ws_bytes: int, stream: int = 0) -> None:
-    _check(lib().sa_kv8_fwd(ctypes.byref(cache), ctypes.byref(query), ws, ws_bytes, stream), "sa_kv8_fwd")
-
-
 def sa_debug_resolve(args: SaArgs, rows: int, counts: int, max_rows: int, stream: int = 0) -> None:
     _check(lib().sa_debug_resolve(ctypes.byref(args), rows, counts, max_rows, stream), "sa_debug_resolve")
 
