@@ -234,6 +234,25 @@ def test_latent_codes_that_begin_between_32_bytes():
     check("moved", o, lse, ref, q.dtype, 576, 150)
 
 
+@pytest.mark.parametrize("topk", [0, 200])
+def test_many_latent_codes_that_begin_between_32_bytes(topk):
+    """The same with tokens enough for that kernel, so that the alignment alone keeps the call off it."""
+    rng = np.random.default_rng(56)
+    lens, new = [333, 64, 129], [10, 6, 9]
+    cu = np.concatenate([[0], np.cumsum(new)])
+    cache, table, kf, vf = make_cache(rng, lens, page=64, H=1, dqk=576, dv=512, shared=True)
+    buf = torch.empty(cache.k.numel() + 16, dtype=torch.uint8, device="cuda")
+    k = buf[16:].view(cache.k.dtype).view(cache.k.shape)
+    k.view(torch.uint8).copy_(cache.k.view(torch.uint8))
+    assert k.data_ptr() % 32 == 16
+    q = torch.randn((25, 64, 576), device="cuda").to(torch.bfloat16)
+    idx = make_idx(rng, lens, new, 1, 1, topk) if topk else None
+    moved = Kv8Cache(k, None, cache.k_scale, None, d_v=512)
+    o, lse = moved.attend(q, _i32(table), _i32(lens), cu_seqlens_q=_i32(cu), idx=_i32(idx) if topk else None)
+    ref = R.attend(q.double().cpu().numpy(), kf, vf, table, lens, cu, 64, 576 ** -0.5, idx=idx)
+    check("moved", o, lse, ref, q.dtype, 576, 333)
+
+
 def test_attend_bsnd_strided_inputs_and_given_outputs():
     rng = np.random.default_rng(5)
     lens, s, H, G, d = [90, 200, 33], 2, 2, 4, 128

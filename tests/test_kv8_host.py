@@ -151,6 +151,28 @@ def test_bad_queries_are_refused(kw, status):
                                                  ctypes.byref(n)) == status
 
 
+@pytest.mark.parametrize("t_q,max_pages,heads,takes", [
+    (25, 6, 64, True),        # 25 tokens x 2 x 6 shares of 32 heads x 64 rows: more than SMs
+    (2, 3, 64, False),        # 12 shares: the kernel with mma.sync at any alignment
+    (25, 6, 32, False),       # up to 32 heads: likewise
+])
+def test_codes_between_32_bytes_take_the_kernel_that_can_read_them(t_q, max_pages, heads, takes):
+    """The tensor-memory kernel reads 32 bytes of codes at a time.  Which kernel a call takes shows in its
+    workspace: a part of a unit is 64 heads there, 32 at most in the other."""
+    size = {}
+    for off in (0, 16, 32):
+        c = _cache(kv_shared=1, d_qk=576, d_v=512, n_heads_kv=1, page_size=64, n_pages=40, max_pages=max_pages,
+                   table_stride=max_pages, t_q=t_q, k=FAKE + off)
+        n = ctypes.c_size_t(0)
+        q = _query(n_heads_q=heads, q_stride=heads * 576)
+        assert L.lib().sa_kv8_fwd_get_workspace_size(ctypes.byref(c), ctypes.byref(q), ctypes.byref(n)) == L.SA_OK
+        size[off] = n.value
+    assert size[32] == size[0] and (size[16] != size[0]) == takes
+    units = t_q * -(-heads // 32)                          # of 32 heads; chunks of 64 rows
+    n_cta = min(148, units * max_pages)
+    assert size[16] == -(-n_cta * 2 * 24 // 256) * 256 + n_cta * 2 * 32 * (2 + 512) * 4
+
+
 def test_workspace_and_null_arguments_are_refused():
     lib, n = L.lib(), ctypes.c_size_t(0)
     assert lib.sa_kv8_fwd_get_workspace_size(None, ctypes.byref(_query()), ctypes.byref(n)) == L.SA_ERR_NULLPTR
