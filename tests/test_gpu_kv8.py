@@ -157,6 +157,17 @@ CASES = {
                        window=200),
     "latents_blocks": dict(lens=[500, 77], new=[14, 14], G=33, H=1, dqk=576, dv=512, shared=True, block=16, topk=13,
                            page=16, fmt="int8"),
+    # the last of several parts of the heads is a small one; pages and windows that cut the chunks of both kernels
+    "latent_40": dict(lens=[90, 300], new=[1, 2], G=40, H=1, dqk=576, dv=512, shared=True, page=7),
+    "latents_100": dict(lens=[500, 77], new=[9, 9], G=100, H=1, dqk=576, dv=512, shared=True, page=7, sinks=True),
+    "latents_rows_window": dict(lens=[500, 77, 260], new=[12, 9, 4], G=64, H=1, dqk=576, dv=512, shared=True, block=1,
+                                topk=300, window=131, dtype="fp16"),
+    "latent_rows_window": dict(lens=[500, 77, 2], new=[2, 1, 2], G=8, H=2, dqk=576, dv=512, shared=True, block=4,
+                               topk=60, window=131, page=16),
+    # whole prompts beside a long request's one token
+    "prompts": dict(lens=[300, 17, 2000], new=[300, 17, 1], G=8, H=1, dqk=128, dv=128),
+    "prompts_mha": dict(lens=[150, 333], new=[150, 33], G=1, H=3, dqk=64, dv=64, fmt="int8", window=64, sinks=True),
+    "prompts_latent": dict(lens=[120, 40], new=[120, 40], G=16, H=1, dqk=576, dv=512, shared=True),
     "shared_128": dict(lens=[500, 33, 8], new=[2, 1, 8], G=32, H=1, dqk=128, dv=128, shared=True, dtype="fp16"),
     "shared_128_blocks": dict(lens=[500, 33], new=[2, 1], G=6, H=2, dqk=128, dv=128, shared=True, block=16, topk=6),
 }
@@ -532,6 +543,106 @@ def test_a_step_without_tokens(shared, dqk, dv, topk, B):
     assert cache.read_status() == L.SA_OK and int(cache.k.view(torch.uint8).max()) == 0
 
 
+LATER = [(False, 8, 128, 128, 0), (False, 8, 192, 128, 3), (True, 16, 576, 512, 40), (True, 128, 576, 512, 40),
+         (True, 64, 576, 512, 0)]
+
+
+@pytest.mark.parametrize("shared,G,dqk,dv,topk", LATER)
+def test_a_captured_step_replays_whatever_its_requests_bring(shared, G, dqk, dv, topk):
+    """Plan, write and attention in one graph, replayed with other lengths each time, none at all among them."""
+    rng = np.random.default_rng(61)
+    B, T, page, mp = 4, 24, 16, 9
+    cache = Kv8Cache.empty(40, page, 1, dqk, dv, shared=shared)
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    old, new, table, free, n_free = z(B), z(B), z(B, mp) - 1, _i32(np.arange(40)), _i32([40])
+    k, v, q = (torch.zeros((T, h, d), dtype=torch.bfloat16, device="cuda") for h, d in ((1, dqk), (1, dv), (G, dqk)))
+    o, lse = torch.zeros((T, G, dv), dtype=torch.bfloat16, device="cuda"), torch.zeros((T, G), device="cuda")
+    idx = z(T, 1, topk) if topk else None
+    block = 1 if shared else 16
+
+    def step():
+        p = plan_pages(old, new, table, free, n_free, page_size=page, n_tokens=T)
+        cache.write(k, None if shared else v, table, p.seq_lens, cu_seqlens_q=p.cu_seqlens_q)
+        cache.attend(q, table, p.seq_lens, cu_seqlens_q=p.cu_seqlens_q, idx=idx, block_size=block, o=o, lse=lse)
+        old.copy_(p.seq_lens)
+        n_free.copy_(p.n_free)
+        return p
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p = step()
+    lens = np.zeros(B, int)
+    for n in ([9, 0, 14, 1], [0, 0, 0, 0], [1, 1, 1, 1], [0, 22, 0, 0], [6, 6, 6, 6]):
+        lens += n
+        for x in (k, v, q):
+            x.copy_(torch.randn(x.shape))
+        new.copy_(_i32(n))
+        if topk:
+            at = np.full((T, 1, topk), 1 << 30)
+            at[:sum(n)] = make_idx(rng, lens.tolist(), n, 1, block, topk)
+            idx.copy_(_i32(at))
+        o.fill_(7)
+        lse.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        t = sum(n)
+        cu = np.concatenate([[0], np.cumsum(n)])
+        assert p.cu_seqlens_q.tolist() == cu.tolist() and old.tolist() == lens.tolist() and int(p.n_served) == B
+        kf, vf = (None if x is None else x.double().cpu().numpy() for x in cache.dequantize())
+        ref = R.attend(q[:t].double().cpu().numpy(), kf, kf[..., :dv] if shared else vf, table.cpu().numpy(), lens, cu, page,
+                       dqk ** -0.5, idx=at[:t] if topk else None, block_size=block)
+        check("step", o[:t], lse[:t], ref, q.dtype, dqk, 200)
+        assert (o[t:] == 7).all() and (lse[t:] == 7).all() and cache.read_status() == L.SA_OK
+
+
+@pytest.mark.parametrize("shared,G,dqk,dv,topk", LATER)
+def test_lengths_beyond_the_table_are_cut_to_it(shared, G, dqk, dv, topk):
+    """seq_lens past max_pages * page_size: the rows that the table holds, in the attention and in the write."""
+    rng = np.random.default_rng(62)
+    lens, n, page = [64, 48], [20, 17], 16
+    cache, table, kf, vf = make_cache(rng, lens, page=page, H=1, dqk=dqk, dv=dv, shared=shared)
+    table, cu = table[:1].repeat(2, 0), _i32(np.concatenate([[0], np.cumsum(n)]))
+    q = torch.randn((sum(n), G, dqk), device="cuda").to(torch.bfloat16)
+    block = 1 if shared else 16
+    idx = make_idx(rng, [64, 64], n, 1, block, topk) if topk else None
+    far = _i32([65, 2 ** 31 - 1])
+    o, lse = cache.attend(q, _i32(table), far, cu_seqlens_q=cu, idx=None if idx is None else _i32(idx), block_size=block)
+    ref = R.attend(q.double().cpu().numpy(), kf, vf, table, [64, 64], cu.tolist(), page, dqk ** -0.5, idx=idx,
+                   block_size=block)
+    check("far", o, lse, ref, q.dtype, dqk, 64)
+    c = dict(lens=[64], new=[20], H=1, dqk=dqk, dv=dv, fmt="e4m3", shared=shared)
+    k, v = (torch.from_numpy(rng.standard_normal((20, 1, d))).to(torch.bfloat16) for d in (dqk, dv))
+    kd, vd = k.cuda(), None if shared else v.cuda()
+    _check_write(c, cache, table[:1], k, v, [0, 20],
+                 lambda: cache.write(kd, vd, _i32(table[:1]), far[1:], cu_seqlens_q=_i32([0, 20])))
+
+
+@pytest.mark.parametrize("shared,G,dqk,dv,topk", LATER)
+def test_calls_on_two_streams_repeat_each_other(shared, G, dqk, dv, topk):
+    """The order of every sum is fixed: the same bits from each call, whatever runs beside it."""
+    rng = np.random.default_rng(63)
+    lens, new = [900, 33, 350, 1, 620], [5, 6, 7, 1, 6]
+    cache, table, _, _ = make_cache(rng, lens, page=16, H=1, dqk=dqk, dv=dv, shared=shared)
+    tab, ln, cu = _i32(table), _i32(lens), _i32(np.concatenate([[0], np.cumsum(new)]))
+    block = 1 if shared else 16
+    idx = _i32(make_idx(rng, lens, new, 1, block, topk)) if topk else None
+    q = torch.randn((sum(new), G, dqk), device="cuda").to(torch.bfloat16)
+    torch.cuda.synchronize()
+    outs, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(cache.attend(q, tab, ln, cu_seqlens_q=cu, idx=idx, block_size=block))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, outs[0][0]) and torch.equal(l, outs[0][1]) for o, l in outs[1:])
+    assert cache.read_status() == L.SA_OK
+
+
 # ---- write --------------------------------------------------------------------
 
 WRITES = {
@@ -724,6 +835,17 @@ def test_plan(B, page, lo, hi, old_hi, short):
         assert np.array_equal(got.cpu().numpy(), ref)
     assert int(p.n_free) == want[4] and int(p.n_served) == want[5]
     assert (want[5] < B) == (short > 0)
+
+
+@pytest.mark.parametrize("B,T", [(0, 0), (0, 5), (3, 0), (3, 300)])
+def test_plan_of_nothing(B, T):
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = z(B, 2) - 1
+    for free, n in ((z(0), 0), (z(4) + 1, 3)):
+        p = plan_pages(z(B) + 7, z(B), table, free, z(1) + n, page_size=16, n_tokens=T)
+        assert p.seq_lens.tolist() == [7] * B and p.cu_seqlens_q.tolist() == [0] * (B + 1)
+        assert p.slots.tolist() == [-1] * T and p.n_free.tolist() == [n] and p.n_served.tolist() == [B]
+        assert (table == -1).all()
 
 
 @pytest.mark.parametrize("what", ["negative_old", "negative_new", "tokens", "max_pages", "huge", "no_free"])
