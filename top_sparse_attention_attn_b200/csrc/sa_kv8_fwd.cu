@@ -39,8 +39,8 @@ bool k8_built(int dqk, int dv, bool shared) {
 // exponential, and its 11 bits sit where the products are largest whatever the pages'
 // scales are.  p' <= 2^15: the maximum is held at 2^7 and let grow by up to 2^8 before O is
 // rescaled; halves reach 2^-31 of the held one.
-// Measured: 32 requests of 8 k to 32 k rows, 64 / 8 heads of 128 / 128, 1.32 GB: 255 to 271 us,
-// 4.9 to 5.2 TB/s of a copy's 6.55; bound by the issue slots close behind memory.  16 requests of
+// Measured: 32 requests of 8 k to 32 k rows, 64 / 8 heads of 128 / 128, 1.32 GB: 273 to 278 us,
+// 4.8 TB/s of a copy's 6.55; bound by the issue slots close behind memory.  16 requests of
 // up to 8 k rows: 43 us, of which start and join are 16.  One of 65536 rows, 4 heads of 192 / 128: 31.
 constexpr int kK8Warps = 4;
 constexpr int kK8Chunk = 32 * kK8Warps;
@@ -953,7 +953,7 @@ __global__ void __launch_bounds__(256) k8_join_kernel(const K8Fwd a, float* ws, 
   __shared__ float sl[8];
   __shared__ float4 so[8][NV * kLanes];
   // No early launch of what comes behind: another attention's CTAs, placed while these still run, end up
-  // unevenly on the SMs (387 instead of 255 us a call, one long decode step behind the other).
+  // unevenly on the SMs (381 instead of 272 us a call, one long decode step behind the other; 59 instead of 43, one decode step).
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll 1
@@ -2048,7 +2048,8 @@ static void k8_geometry(K8Fwd& a) {
   a.by_gdiv = k8_div_of(a.gdiv);
   // Units of one length, and no more than SMs: as many CTAs each as there are, of which none has parts of two
   // units.  A part's start, end and join (131 KB of 64 heads x 512) cost as much as 5 chunks of 64 heads.  With 2048 rows:
-  // 37 against 45 us of the even cut (48 tokens, 16 heads), 59 against 71 (40, 64), 96 against 106 (48, 128).
+  // 37 against 45 us of the even cut (48 tokens, 16 heads), 59 against 71 (40, 64), 96 against 106 (48, 128).  Only
+  // 2048 rows were measured: with many more, a whole unit's chunks on one CTA outweigh what a part costs.
   const long long units = (long long)a.c.T * a.hs * a.c.Hkv;
   a.per_unit = lat && a.topk && units <= 148 && a.sel_ch < 1 << 20 ? min(148 / (int)units, a.sel_ch) : 0;
   a.by_ch = k8_div_of(max(a.sel_ch, 1));

@@ -15,7 +15,7 @@ namespace sa {
 // from L2) into two prefix arrays in shared memory, tokens and new pages, and then
 // looks up its share of the tokens and new pages there by bisection; block 0 writes
 // the per-request outputs.  The scan repeated per block costs less than a second
-// launch that would wait for it.  Bound by latency: 6.4 us for 64 requests, 7.2 for 1500.
+// launch that would wait for it.  Bound by latency: 6.4 us for 64 requests, 7.3 for 1500.
 __device__ __forceinline__ int plan_upper(const int* a, int n, int x) {  // largest b < n with a[b] <= x
   int lo = 0, hi = n - 1;
   while (lo < hi) {
@@ -316,7 +316,7 @@ __device__ __forceinline__ int k8_find_warp(const K8Cache& c, int t, int lane) {
 // of the grid's x range find run x over the requests' page counts.  Bound by the bytes (2
 // in, 1 out per element) and, a run at a time, by the chain offsets -> rows -> maximum ->
 // codes; CTAs enough that an SM holds several.  10 k tokens of 7 prompts, 4 heads of 192 / 128:
-// 13.1 us, 2.9 TB/s.
+// 13.2 us, 2.9 TB/s.
 template <bool F16, int NT>
 __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 6) kv8_write_runs_kernel(const __grid_constant__ K8Write a) {
   __shared__ float red[NT / 32];
