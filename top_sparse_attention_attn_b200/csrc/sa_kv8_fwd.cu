@@ -500,7 +500,9 @@ __global__ void __launch_bounds__(128, K8Split<DK, DV, ROWS, FMT>::kOcc)
     const int last = ROWS ? row : row + 15;
     return row < u.hi && last >= u.lo ? row : -1;
   };
-  auto fetch_page = [&](int un, int row) -> int { return row >= 0 ? k8_read(units[un].table + k8_quot(c.by_ps, row)) : 0; };
+  auto fetch_page = [&](int un, int row) -> int {
+    return row >= 0 ? k8_read(units[un].table + k8_quot(c.by_ps, row)) : 0;
+  };
   int fx = 0, f_row = -1, f_page = 0, f_head = 0;
   // the page of the step that the fetch stands at, then the index of the one behind it
   auto look = [&]() {
@@ -953,7 +955,8 @@ __global__ void __launch_bounds__(256) k8_join_kernel(const K8Fwd a, float* ws, 
   __shared__ float sl[8];
   __shared__ float4 so[8][NV * kLanes];
   // No early launch of what comes behind: another attention's CTAs, placed while these still run, end up
-  // unevenly on the SMs (381 instead of 272 us a call, one long decode step behind the other; 59 instead of 43, one decode step).
+  // unevenly on the SMs (381 instead of 272 us a call, one long decode step behind the other; 59 instead of 43,
+  // one decode step).
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll 1
